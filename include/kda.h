@@ -102,13 +102,14 @@ enum {
   KDA_SCAN_LOGDEPTH = 1u << 7, /* segment call: the scan in log depth (needs the workspace of
                                   kda_scan_workspace_size); without it the log-depth form is
                                   chosen when that workspace is given and it is expected faster */
-  KDA_DEBUG_WITHHOLD_HANDOFF = 1u << 8 /* test hook for the bounded waits (kda_chunk_fwd): the bf16
+  KDA_DEBUG_WITHHOLD_HANDOFF = 1u << 8, /* test hook for the bounded waits (kda_chunk_fwd): the bf16
                                   kernel withholds one "scores ready" signal between its two
                                   warp teams in every chain's first chunk, so the waiting team
                                   gives up after its limit (about one second).  device_status
                                   then reads KDA_ERR_DEVICE_TIMEOUT, the outputs and the pool
                                   slots are unspecified, and the context stays usable.  No
                                   effect on the fp32 kernel. */
+  KDA_INPUT_NORM = 1u << 9     /* kda_glr_*: the input is scaled by sqrt(1 - a^2)                */
 };
 
 /*
@@ -450,6 +451,150 @@ KDA_API const char *kda_status_string(kda_status_t status);
 
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
 KDA_API int32_t kda_version(void);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * The gated linear recurrence: the diagonal-state relative of KDA, for stacks that mix both kinds
+ * of layer.  Same forget gate, same per-head beta, same varlen and pool conventions; the state is
+ * one number per channel.  For every sequence, head h, channel c and token t:
+ *     g = -exp(a_log[h]) softplus(raw_gate[t,h,c] + dt_bias[h,c])   (safe: max(g, lower bound))
+ *     a = exp(g),  b = beta x[t,h,c]  (KDA_INPUT_NORM: b = beta sqrt(1 - a^2) x)
+ *     state = a state + b,  out[t,h,c] = state
+ * with beta = sigmoid(beta_logits[t,h]), or beta_logits itself with KDA_BETA_PROB.
+ *
+ *   x          [total_tokens, num_heads, d]  x_dtype
+ *   raw_gate   [total_tokens, num_heads, d]  gate_dtype
+ *   beta_logits [total_tokens, num_heads], a_log [num_heads], dt_bias [num_heads, d]   fp32
+ *   state_pool [max_slots, num_heads, d]     fp32, read and written in place
+ *   out        [total_tokens, num_heads, d]  out_dtype
+ * Types: x F32 with gate F32 and out F32; or x BF16 with gate BF16 or F32 and out BF16 or F32.
+ * 1 <= d <= 128.  Any alignment of whole elements; rows of a multiple of four channels on 16-byte
+ * (bf16: 8-byte) boundaries are read and written in wide accesses.
+ * flags: KDA_GATE_SAFE, KDA_BETA_PROB, KDA_INPUT_NORM.  Arithmetic and states in fp32; results do
+ * not depend on timing.
+ */
+KDA_API kda_status_t kda_glr_fwd(const void *x, kda_dtype_t x_dtype, const void *raw_gate,
+                                 kda_dtype_t gate_dtype, const float *beta_logits, const float *a_log,
+                                 const float *dt_bias, const int32_t *cu_seqlens, int32_t batch,
+                                 int64_t total_tokens, int32_t num_heads, int32_t d, float *state_pool,
+                                 int32_t max_slots, const int32_t *state_indices, void *out,
+                                 kda_dtype_t out_dtype, float *checkpoints, uint32_t flags,
+                                 float gate_lower_bound, int32_t *device_status, void *stream);
+/* checkpoints (nullable): [kda_glr_checkpoints(total_tokens, batch), num_heads, d] fp32, written:
+ * the state entering every 64th token of each sequence (entry cu_seqlens[b] / 64 + b + j for
+ * sequence b's tokens from 64 j on; entries that no token needs are not written), which
+ * kda_glr_bwd reads. */
+KDA_API int64_t kda_glr_checkpoints(int64_t total_tokens, int32_t batch);
+
+/* One token of each sequence: x, raw_gate, out [batch, num_heads, d], beta_logits [batch, num_heads].
+ * Equals kda_glr_fwd on sequences of one token each. */
+KDA_API kda_status_t kda_glr_decode(const void *x, kda_dtype_t x_dtype, const void *raw_gate,
+                                    kda_dtype_t gate_dtype, const float *beta_logits, const float *a_log,
+                                    const float *dt_bias, int32_t batch, int32_t num_heads, int32_t d,
+                                    float *state_pool, int32_t max_slots, const int32_t *state_indices,
+                                    void *out, kda_dtype_t out_dtype, uint32_t flags, float gate_lower_bound,
+                                    int32_t *device_status, void *stream);
+
+/*
+ * kda_glr_bwd -- the gradients of kda_glr_fwd, for the same inputs, flags and bound.
+ *   dout         [total_tokens, num_heads, d]  out_dtype (the forward pass's)
+ *   checkpoints  as kda_glr_fwd wrote them
+ *   d_final      [batch, num_heads, d] fp32, nullable (zero): gradient of each sequence's final state
+ *   dx, draw_gate  as x and raw_gate, written;  dbeta [total_tokens, num_heads] fp32, of beta_logits
+ *   da_log [num_heads], ddt_bias [num_heads, d] fp32, summed over all tokens
+ *   d_initial    [batch, num_heads, d] fp32: gradient of the state each sequence started from
+ * A gate at or below the safe bound passes no gradient.  Rows of tokens outside every sequence are
+ * left as they were.  workspace: at least kda_glr_bwd_workspace_size() bytes, 256-byte aligned, on
+ * the current device; calls that may run at once need one each.
+ */
+KDA_API kda_status_t kda_glr_bwd(const void *dout, kda_dtype_t out_dtype, const void *x, kda_dtype_t x_dtype,
+                                 const void *raw_gate, kda_dtype_t gate_dtype, const float *beta_logits,
+                                 const float *a_log, const float *dt_bias, const int32_t *cu_seqlens,
+                                 int32_t batch, int64_t total_tokens, int32_t num_heads, int32_t d,
+                                 const float *checkpoints, const float *d_final, void *dx, void *draw_gate,
+                                 float *dbeta, float *da_log, float *ddt_bias, float *d_initial,
+                                 uint32_t flags, float gate_lower_bound, void *workspace,
+                                 size_t workspace_bytes, int32_t *device_status, void *stream);
+KDA_API size_t kda_glr_bwd_workspace_size(int64_t total_tokens, int32_t batch, int32_t num_heads, int32_t d);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * kda_tree_decode -- KDA over a tree of drafted tokens per sequence, against its state in the pool.
+ * Sequence b drafts the nodes cu_nodes[b] .. cu_nodes[b+1] - 1; parents[i] is the node's parent,
+ * numbered within the sequence and smaller than the node's own number, or -1 where the node follows
+ * the state itself.  Every node's output equals kda_decode's after its ancestors' tokens from the
+ * root down and its own, and the pool is only read.
+ *
+ *   q, k [total_nodes, num_k_heads, dk], v [total_nodes, num_v_heads, dv]   qkv_dtype
+ *   raw_gate [total_nodes, num_v_heads, dk], beta_logits [total_nodes, num_v_heads],
+ *   a_log [num_v_heads], dt_bias [num_v_heads, dk]   fp32, as kda_decode
+ *   cu_nodes [batch + 1], parents [total_nodes], state_indices [batch]   int32
+ *   state_pool  as kda_decode (K_FIRST or V_FIRST)
+ *   out    [total_nodes, num_v_heads, dv] out_dtype
+ *   deltas [total_nodes, num_v_heads, dv] fp32: beta (v - k^T S) of every node, the value it writes
+ *          along its key; kda_tree_commit reads them
+ *   max_nodes (1 .. 64): no sequence drafts more; one that does is reported and skipped, as are
+ *          bad offsets, a bad slot and a parent outside [-1, node)
+ * Types and head sizes as kda_decode; fp32-accurate arithmetic.
+ */
+KDA_API kda_status_t kda_tree_decode(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,
+                                     const float *raw_gate, const float *beta_logits, const float *a_log,
+                                     const float *dt_bias, const int32_t *cu_nodes, const int32_t *parents,
+                                     int32_t batch, int64_t total_nodes, int32_t max_nodes,
+                                     int32_t num_k_heads, int32_t num_v_heads, int32_t dk, int32_t dv,
+                                     const float *state_pool, int32_t max_slots, const int32_t *state_indices,
+                                     void *out, kda_dtype_t out_dtype, float *deltas, uint32_t flags,
+                                     float gate_lower_bound, int32_t *device_status, void *stream);
+
+/* kda_tree_commit -- the accepted path of each tree written into the sequence's slot, in place:
+ * the state after the tokens from the root down to node accepted[b] (numbered within the sequence;
+ * -1: nothing was accepted, and the slot stays as it is).  k, raw_gate, cu_nodes, parents and deltas
+ * as in kda_tree_decode; an accepted node outside the tree is reported and the slot left alone. */
+KDA_API kda_status_t kda_tree_commit(const void *k, kda_dtype_t k_dtype, const float *raw_gate,
+                                     const float *a_log, const float *dt_bias, const float *deltas,
+                                     const int32_t *cu_nodes, const int32_t *parents, const int32_t *accepted,
+                                     int32_t batch, int64_t total_nodes, int32_t max_nodes,
+                                     int32_t num_k_heads, int32_t num_v_heads, int32_t dk, int32_t dv,
+                                     float *state_pool, int32_t max_slots, const int32_t *state_indices,
+                                     uint32_t flags, float gate_lower_bound, int32_t *device_status,
+                                     void *stream);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Slots of a state pool moved about: state_pool [layers, max_slots, slot_elems] fp32 (KDA's pool or
+ * the recurrence's; slot_elems counts everything behind the slot's index, layers stacks the pools of
+ * several layers that share their indices).  Everything is decided on the device, so the calls can
+ * be captured.  live [max_slots] int32: nonzero where a slot is in use.  workspace: at least
+ * kda_pool_workspace_size(n, max_slots) bytes, 256-byte aligned; calls that may run at once need one
+ * each.  Entries of -1 in the lists (both, for a copy) are padding.
+ *
+ * kda_pool_copy     slot dst[i] = slot src[i] for all i at once: sources are read as they were before
+ *                   the call, whatever the order.  A destination named again is reported and only its
+ *                   first pair counts.  n <= 8192.
+ * kda_pool_fork     every src[i] copied to a slot of its own, dst[i] (written): the lowest free ones in
+ *                   the order of the list, then marked live.  A source that is not live, or one too
+ *                   many, is reported and gets -1.
+ * kda_pool_free     the listed slots marked free and cleared (a sequence starts from zero).  One that
+ *                   is not live, or is listed again, is reported and left alone.
+ * kda_pool_compact  live slots moved down so that they fill 0 .. num_live - 1: the j-th empty slot
+ *                   there receives the j-th live slot above.  state_indices [n] and live follow;
+ *                   num_live [1] is written.  Contents of the slots left behind are unspecified.  An
+ *                   index that names no live slot is reported and kept.
+ */
+KDA_API size_t kda_pool_workspace_size(int32_t n, int32_t max_slots);
+KDA_API kda_status_t kda_pool_copy(float *state_pool, int32_t layers, int32_t max_slots, int64_t slot_elems,
+                                   const int32_t *src, const int32_t *dst, int32_t n, void *workspace,
+                                   size_t workspace_bytes, int32_t *device_status, void *stream);
+KDA_API kda_status_t kda_pool_fork(float *state_pool, int32_t layers, int32_t max_slots, int64_t slot_elems,
+                                   int32_t *live, const int32_t *src, int32_t *dst, int32_t n, void *workspace,
+                                   size_t workspace_bytes, int32_t *device_status, void *stream);
+KDA_API kda_status_t kda_pool_free(float *state_pool, int32_t layers, int32_t max_slots, int64_t slot_elems,
+                                   int32_t *live, const int32_t *slots, int32_t n, void *workspace,
+                                   size_t workspace_bytes, int32_t *device_status, void *stream);
+KDA_API kda_status_t kda_pool_compact(float *state_pool, int32_t layers, int32_t max_slots, int64_t slot_elems,
+                                      int32_t *live, int32_t *state_indices, int32_t n, int32_t *num_live,
+                                      void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                      void *stream);
 
 #ifdef __cplusplus
 }

@@ -17,9 +17,13 @@ Public calls (same names as the C ABI):
   kda_context_parallel_range_finish(...)  that range's outputs from the state entering it
                                           (``distributed.context_parallel_prefill`` joins the
                                           two across ranks with one all-gather)
+  kda_glr_fwd / kda_glr_bwd / kda_glr_decode   the gated linear recurrence (``glr``)
+  kda_tree_decode / kda_tree_commit            trees of drafted tokens against the states (``tree``)
+  kda_pool_copy / _fork / _free / _compact     slots of a state pool moved about (``pool``)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -31,6 +35,10 @@ __all__ = ["kda_chunk_fwd", "kda_decode", "kda_segment_summarize_and_scan", "kda
            "kda_context_parallel_piece_offsets", "kda_segment_compose", "kda_context_parallel_range_workspace_size",
            "kda_context_parallel_range_summary", "kda_context_parallel_range_finish", "kda_prefill_host_pipelined",
            "kda_prefill_host_workspace_size", "kda_workspace_size",
+           "kda_glr_fwd", "kda_glr_bwd", "kda_glr_decode", "kda_glr_checkpoint_shape", "kda_glr_bwd_workspace_size",
+           "kda_tree_decode", "kda_tree_commit", "MAX_TREE_NODES",
+           "kda_pool_copy", "kda_pool_fork", "kda_pool_free", "kda_pool_compact", "kda_pool_workspace_size",
+           "MAX_POOL_COPIES",
            "kda_status_string", "load_library", "KdaError", "LIB_PATH"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -121,6 +129,11 @@ def load_library():
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_version.restype = i32
     lib.kda_version.argtypes = []
+    from . import glr, pool, tree
+    for module in (glr, tree, pool):
+        for name, (restype, argtypes) in module.SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = restype, argtypes
     _lib = lib
     return lib
 
@@ -188,6 +201,13 @@ def _stream(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _on_device(device):
+    """Makes ``device`` the current one for a launch, at no cost where it already is."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 class _Owned:
@@ -830,3 +850,8 @@ def kda_prefill_host_pipelined(q, k, v, raw_gate, beta_logits, a_log, dt_bias, i
     if rc != 0:
         raise KdaError(rc, "kda_prefill_host_pipelined")
     return {"out": out, "final_state": final_state}
+
+
+from .glr import *  # noqa: E402,F401,F403
+from .pool import *  # noqa: E402,F401,F403
+from .tree import *  # noqa: E402,F401,F403

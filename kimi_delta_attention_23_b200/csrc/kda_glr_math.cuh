@@ -1,0 +1,157 @@
+// kda_glr_math.cuh -- the gate of the gated linear recurrence in packed two-lane fp32 arithmetic.
+//
+// The forward pass at HBM speed has about 13 issue slots and 6 MUFU cycles per element and SM
+// sub-core to spend, so the gate is evaluated two channels at a time (fma.rn.f32x2 and friends)
+// with two MUFU operations per element: e = 2^(-|z| log2 e) and a = 2^(g log2 e).  softplus(z) =
+// max(z, 0) + log1p(e) takes log1p as e times a degree-9 polynomial: a logarithm of the rounded
+// 1 + e would lose the gates of slow channels (softplus << 1), whose decays multiply up over
+// thousands of tokens.
+//
+// Both polynomials are weighted least-squares fits on Chebyshev nodes made for this file, with the
+// largest relative error of their fp32 Horner evaluation beside them.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace glr {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kTiny = 1.17549435e-38f;  // the smallest normal fp32
+
+__device__ __forceinline__ uint64_t as_u64(float2 x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
+  return r;
+}
+__device__ __forceinline__ float2 as_f2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rsq(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// log1p(e) / e for e in [0, 1] (relative error 1.2e-7)
+__device__ __forceinline__ float2 log1p_ratio(float2 e) {
+  float2 p = both(-0.0032439807f);
+  p = fma2(p, e, both(0.0198512617f));
+  p = fma2(p, e, both(-0.0569591597f));
+  p = fma2(p, e, both(0.106036171f));
+  p = fma2(p, e, both(-0.153055698f));
+  p = fma2(p, e, both(0.196759313f));
+  p = fma2(p, e, both(-0.249541327f));
+  p = fma2(p, e, both(0.333299637f));
+  p = fma2(p, e, both(-0.499999017f));
+  return fma2(p, e, both(1.f));
+}
+
+// expm1(y) / y for y in [-1/2, 0] (relative error 5.4e-8)
+__device__ __forceinline__ float2 expm1_ratio(float2 y) {
+  float2 p = both(0.00112163462f);
+  p = fma2(p, y, both(0.00818738528f));
+  p = fma2(p, y, both(0.0416290872f));
+  p = fma2(p, y, both(0.166662246f));
+  p = fma2(p, y, both(0.499999821f));
+  return fma2(p, y, both(1.f));
+}
+
+// What one head's gate needs besides the pre-activation: -exp(a_log) log2 e, and the safe gate's
+// bound times log2 e (-inf when there is none).
+struct HeadGate {
+  float c2, lb2;
+};
+__device__ __forceinline__ HeadGate head_gate(float a_log, bool safe, float lb) {
+  return {-expf(a_log) * kLog2e, safe ? lb * kLog2e : -INFINITY};
+}
+
+// e = exp(-|z|)
+__device__ __forceinline__ float2 exp_neg_abs(float2 z) {
+  return make_float2(ex2(-fabsf(z.x) * kLog2e), ex2(-fabsf(z.y) * kLog2e));
+}
+// g log2 e before the clamp, from z and e
+__device__ __forceinline__ float2 gate_log2(float2 z, float2 e, float c2) {
+  const float2 sp = fma2(e, log1p_ratio(e), make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+  return mul2(both(c2), sp);
+}
+__device__ __forceinline__ float2 clamp2(float2 g2, float lb2) {
+  return make_float2(fmaxf(g2.x, lb2), fmaxf(g2.y, lb2));
+}
+
+// 1 - a^2 for a = 2^g2: -expm1(2 g) by its polynomial where a^2 >= e^(-1/2), since the difference
+// loses what slow channels are made of there
+__device__ __forceinline__ float2 one_minus_sq(float2 g2, float2 a) {
+  const float2 y = mul2(g2, both(2.f * kLn2));
+  const float2 near = mul2(mul2(y, both(-1.f)), expm1_ratio(y));
+  const float2 far = fma2(mul2(a, both(-1.f)), a, both(1.f));
+  return make_float2(y.x > -0.5f ? near.x : far.x, y.y > -0.5f ? near.y : far.y);
+}
+// 1 / sqrt(u), and sqrt(u) = u / sqrt(u); both 0 below the normal range (nothing is let in there,
+// and the gradient's limit is 0).  One Newton step takes the approximate reciprocal root to fp32 accuracy.
+__device__ __forceinline__ void roots(float2 u, float2& r, float2& s) {
+  const float2 r0 = make_float2(u.x > kTiny ? rsq(u.x) : 0.f, u.y > kTiny ? rsq(u.y) : 0.f);
+  const float2 h = mul2(mul2(u, both(-0.5f)), r0);
+  r = mul2(r0, fma2(h, r0, both(1.5f)));
+  s = mul2(u, r);
+}
+
+// four consecutive channels of an input row in shared or global memory
+__device__ __forceinline__ void unpack4(const __nv_bfloat16* p, float2& lo, float2& hi) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  lo = make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+  hi = make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack4(const float* p, float2& lo, float2& hi) {
+  const float4 w = *reinterpret_cast<const float4*>(p);
+  lo = make_float2(w.x, w.y);
+  hi = make_float2(w.z, w.w);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float2 x) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
+  return r;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float2 lo, float2 hi) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(lo), pack_bf16(hi));
+}
+__device__ __forceinline__ void store4(float* p, float2 lo, float2 hi) {
+  *reinterpret_cast<float4*>(p) = make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
+
+}  // namespace glr
+}  // namespace kda

@@ -1,0 +1,211 @@
+"""The gated linear recurrence: prefill, gradients and the single-token step.
+
+The diagonal-state relative of KDA (one number of state per channel instead of a dk x dv block), with
+the same forget gate, the same per-head beta and the same varlen and pool conventions.  For every
+sequence, head, channel and token
+
+    g = -exp(a_log) * softplus(raw_gate + dt_bias)        (gate_mode "safe": max(g, gate_lower_bound))
+    a = exp(g)
+    state = a * state + beta * s * x                      s = 1, or sqrt(1 - a^2) with input_mode "norm"
+    out = state
+
+with beta = sigmoid(beta_logits), or beta_logits itself with beta_mode "probability".  Types: x float32
+with raw_gate and out float32; or x bfloat16 with raw_gate and out each bfloat16 or float32.  States,
+parameters, beta and the sums over tokens are float32.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (_DTYPES, KdaError, _dev, _flags, _on_device, _Owned, _ptr, _shape, _stream, load_library)
+
+__all__ = ["kda_glr_fwd", "kda_glr_bwd", "kda_glr_decode", "kda_glr_checkpoint_shape", "kda_glr_bwd_workspace_size"]
+
+INPUT_NORM = 1 << 9  # flag bit of include/kda.h
+
+_vp, _i32, _i64, _u32, _f32, _sz, _int = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
+                                          ctypes.c_float, ctypes.c_size_t, ctypes.c_int)
+SIGNATURES = {
+    "kda_glr_fwd": (_int, [_vp, _int, _vp, _int, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _int,
+                           _vp, _u32, _f32, _vp, _vp]),
+    "kda_glr_decode": (_int, [_vp, _int, _vp, _int, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _int, _u32,
+                              _f32, _vp, _vp]),
+    "kda_glr_bwd": (_int, [_vp, _int, _vp, _int, _vp, _int, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp,
+                           _vp, _vp, _vp, _vp, _vp, _u32, _f32, _vp, _sz, _vp, _vp]),
+    "kda_glr_bwd_workspace_size": (_sz, [_i64, _i32, _i32, _i32]),
+    "kda_glr_checkpoints": (_i64, [_i64, _i32]),
+}
+
+
+def kda_glr_checkpoint_shape(total_tokens, batch, num_heads, d):
+    """Shape of the float32 ``checkpoints`` tensor that kda_glr_fwd fills and kda_glr_bwd reads."""
+    return (int(load_library().kda_glr_checkpoints(total_tokens, batch)), num_heads, d)
+
+
+def kda_glr_bwd_workspace_size(total_tokens, batch, num_heads, d) -> int:
+    """Workspace bytes of kda_glr_bwd on the current device."""
+    return int(load_library().kda_glr_bwd_workspace_size(total_tokens, batch, num_heads, d))
+
+
+def _glr_flags(gate_mode, beta_mode, input_mode):
+    if input_mode not in ("unit", "norm"):
+        raise ValueError(f"input_mode must be 'unit' or 'norm', got {input_mode!r}")
+    return _flags(gate_mode, beta_mode, "K_FIRST") | (INPUT_NORM if input_mode == "norm" else 0)
+
+
+def _inputs(x, raw_gate, beta_logits, a_log, dt_bias):
+    """Checks what all three calls read; returns the device and x's shape."""
+    dev = _dev(x, "x").device
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be float32 or bfloat16")
+    if x.dim() != 3:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [tokens, heads, d]")
+    T, H, d = x.shape
+    _shape(_dev(raw_gate, "raw_gate", None, dev), "raw_gate", (T, H, d))
+    if raw_gate.dtype not in _DTYPES or (x.dtype == torch.float32 and raw_gate.dtype != torch.float32):
+        raise ValueError("raw_gate must be float32, or bfloat16 beside a bfloat16 x")
+    _shape(_dev(beta_logits, "beta_logits", torch.float32, dev), "beta_logits", (T, H))
+    _shape(_dev(a_log, "a_log", torch.float32, dev), "a_log", (H,))
+    _shape(_dev(dt_bias, "dt_bias", torch.float32, dev), "dt_bias", (H, d))
+    return dev, T, H, d
+
+
+def _pool(state_pool, state_indices, dev, B, H, d):
+    _dev(state_pool, "state_pool", torch.float32, dev)
+    if state_pool.dim() != 3 or tuple(state_pool.shape[1:]) != (H, d):
+        raise ValueError(f"state_pool has shape {tuple(state_pool.shape)}, expected [slots, {H}, {d}]")
+    _shape(_dev(state_indices, "state_indices", torch.int32, dev), "state_indices", (B,))
+
+
+def _output(out, output_dtype, x, own):
+    if output_dtype is None:
+        output_dtype = x.dtype if out is None else out.dtype
+    if output_dtype not in _DTYPES or (x.dtype == torch.float32 and output_dtype != torch.float32):
+        raise ValueError("output_dtype must be float32, or bfloat16 beside a bfloat16 x")
+    if out is None:
+        out = own.empty(x.shape, dtype=output_dtype, device=x.device)
+    _shape(_dev(out, "out", output_dtype, x.device), "out", x.shape)
+    return out
+
+
+def _status(device_status, dev):
+    if device_status is not None:
+        _shape(_dev(device_status, "device_status", torch.int32, dev), "device_status", (1,))
+
+
+def kda_glr_fwd(x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices, out=None, *,
+                output_dtype=None, checkpoints=None, gate_mode="original", beta_mode="logits", input_mode="unit",
+                gate_lower_bound=-5.0, device_status=None, stream=None):
+    """The recurrence over a varlen batch, states read from and written to their pool slots.
+
+    Shapes: x, raw_gate [T,H,d]; beta_logits [T,H] f32; a_log [H] f32; dt_bias [H,d] f32; cu_seqlens
+    [B+1] i32; state_pool [slots,H,d] f32, mutated in place; state_indices [B] i32.  Returns out
+    [T,H,d] in ``output_dtype`` (default: the dtype of x); rows outside every sequence are not written.
+    ``checkpoints`` (f32, kda_glr_checkpoint_shape(T, B, H, d)) keeps what kda_glr_bwd needs.
+    """
+    lib = load_library()
+    dev, T, H, d = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    own = _Owned(stream, dev)
+    _dev(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold B + 1 offsets")
+    B = cu_seqlens.numel() - 1
+    _pool(state_pool, state_indices, dev, B, H, d)
+    out = _output(out, output_dtype, x, own)
+    if checkpoints is not None:
+        _shape(_dev(checkpoints, "checkpoints", torch.float32, dev), "checkpoints",
+               (lib.kda_glr_checkpoints(T, B), H, d))
+    _status(device_status, dev)
+    flags = _glr_flags(gate_mode, beta_mode, input_mode)
+    with _on_device(dev):
+        rc = lib.kda_glr_fwd(_ptr(x), _DTYPES[x.dtype], _ptr(raw_gate), _DTYPES[raw_gate.dtype], _ptr(beta_logits),
+                             _ptr(a_log), _ptr(dt_bias), _ptr(cu_seqlens), B, T, H, d, _ptr(state_pool),
+                             state_pool.shape[0], _ptr(state_indices), _ptr(out), _DTYPES[out.dtype],
+                             _ptr(checkpoints), flags, float(gate_lower_bound), _ptr(device_status),
+                             _stream(stream, dev))
+    own.launched()
+    if rc != 0:
+        raise KdaError(rc, "kda_glr_fwd")
+    return out
+
+
+def kda_glr_decode(x, raw_gate, beta_logits, a_log, dt_bias, state_pool, state_indices, out=None, *, output_dtype=None,
+                   gate_mode="original", beta_mode="logits", input_mode="unit", gate_lower_bound=-5.0,
+                   device_status=None, stream=None):
+    """One token of each sequence: x, raw_gate [B,H,d]; beta_logits [B,H]; the rest as kda_glr_fwd."""
+    lib = load_library()
+    dev, B, H, d = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    own = _Owned(stream, dev)
+    _pool(state_pool, state_indices, dev, B, H, d)
+    out = _output(out, output_dtype, x, own)
+    _status(device_status, dev)
+    flags = _glr_flags(gate_mode, beta_mode, input_mode)
+    with _on_device(dev):
+        rc = lib.kda_glr_decode(_ptr(x), _DTYPES[x.dtype], _ptr(raw_gate), _DTYPES[raw_gate.dtype], _ptr(beta_logits),
+                                _ptr(a_log), _ptr(dt_bias), B, H, d, _ptr(state_pool), state_pool.shape[0],
+                                _ptr(state_indices), _ptr(out), _DTYPES[out.dtype], flags, float(gate_lower_bound),
+                                _ptr(device_status), _stream(stream, dev))
+    own.launched()
+    if rc != 0:
+        raise KdaError(rc, "kda_glr_decode")
+    return out
+
+
+def kda_glr_bwd(dout, x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, checkpoints, d_final=None, *, dx=None,
+                draw_gate=None, dbeta=None, da_log=None, ddt_bias=None, d_initial=None, gate_mode="original",
+                beta_mode="logits", input_mode="unit", gate_lower_bound=-5.0, workspace=None, device_status=None,
+                stream=None):
+    """Gradients of kda_glr_fwd for the same inputs, modes and bound.
+
+    ``dout`` [T,H,d] in the forward pass's output dtype; ``checkpoints`` as kda_glr_fwd filled them;
+    ``d_final`` [B,H,d] f32 (None: zero) the gradient of each sequence's final state.  Returns
+    dict(dx, draw_gate, dbeta, da_log, ddt_bias, d_initial): in the shapes and dtypes of x, raw_gate,
+    beta_logits, a_log and dt_bias, and [B,H,d] f32 for the states the sequences started from.
+    Tensors to fill can be given; rows outside every sequence are left as they are in those, and
+    unwritten in new ones.  ``workspace``: uint8 CUDA tensor of kda_glr_bwd_workspace_size bytes,
+    allocated when not given.
+    """
+    lib = load_library()
+    dev, T, H, d = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    own = _Owned(stream, dev)
+    _shape(_dev(dout, "dout", None, dev), "dout", (T, H, d))
+    if dout.dtype not in _DTYPES or (x.dtype == torch.float32 and dout.dtype != torch.float32):
+        raise ValueError("dout must be float32, or bfloat16 beside a bfloat16 x")
+    _dev(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold B + 1 offsets")
+    B = cu_seqlens.numel() - 1
+    _shape(_dev(checkpoints, "checkpoints", torch.float32, dev), "checkpoints", (lib.kda_glr_checkpoints(T, B), H, d))
+    if d_final is not None:
+        _shape(_dev(d_final, "d_final", torch.float32, dev), "d_final", (B, H, d))
+
+    def grad(t, name, shape, dtype=torch.float32):
+        if t is None:
+            return own.empty(shape, dtype=dtype, device=dev)
+        _shape(_dev(t, name, dtype, dev), name, shape)
+        return t
+
+    dx = grad(dx, "dx", (T, H, d), x.dtype)
+    draw_gate = grad(draw_gate, "draw_gate", (T, H, d), raw_gate.dtype)
+    dbeta = grad(dbeta, "dbeta", (T, H))
+    da_log = grad(da_log, "da_log", (H,))
+    ddt_bias = grad(ddt_bias, "ddt_bias", (H, d))
+    d_initial = grad(d_initial, "d_initial", (B, H, d))
+    _status(device_status, dev)
+    flags = _glr_flags(gate_mode, beta_mode, input_mode)
+    with _on_device(dev):
+        if workspace is None:
+            workspace = own.empty(lib.kda_glr_bwd_workspace_size(T, B, H, d), dtype=torch.uint8, device=dev)
+        _dev(workspace, "workspace", torch.uint8, dev)
+        rc = lib.kda_glr_bwd(_ptr(dout), _DTYPES[dout.dtype], _ptr(x), _DTYPES[x.dtype], _ptr(raw_gate),
+                             _DTYPES[raw_gate.dtype], _ptr(beta_logits), _ptr(a_log), _ptr(dt_bias), _ptr(cu_seqlens),
+                             B, T, H, d, _ptr(checkpoints), _ptr(d_final), _ptr(dx), _ptr(draw_gate), _ptr(dbeta),
+                             _ptr(da_log), _ptr(ddt_bias), _ptr(d_initial), flags, float(gate_lower_bound),
+                             _ptr(workspace), workspace.numel(), _ptr(device_status), _stream(stream, dev))
+    own.launched()
+    if rc != 0:
+        raise KdaError(rc, "kda_glr_bwd")
+    return {"dx": dx, "draw_gate": draw_gate, "dbeta": dbeta, "da_log": da_log, "ddt_bias": ddt_bias,
+            "d_initial": d_initial}
