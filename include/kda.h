@@ -468,7 +468,7 @@ KDA_API int32_t kda_version(void);
  *   state_pool [max_slots, num_heads, d]     fp32, read and written in place
  *   out        [total_tokens, num_heads, d]  out_dtype
  * Types: x F32 with gate F32 and out F32; or x BF16 with gate BF16 or F32 and out BF16 or F32.
- * 1 <= d <= 128.  Any alignment of whole elements; rows of a multiple of four channels on 16-byte
+ * 1 <= d <= 128; total_tokens at most 2^31 - 1025.  Any alignment of whole elements; rows of a multiple of four channels on 16-byte
  * (bf16: 8-byte) boundaries are read and written in wide accesses.
  * flags: KDA_GATE_SAFE, KDA_BETA_PROB, KDA_INPUT_NORM.  Arithmetic and states in fp32; results do
  * not depend on timing.

@@ -23,10 +23,12 @@
 // tile (1/64 of the fp32 size of the outputs), so h_{t-1} is rebuilt inside the tile and only D is
 // carried.
 #include <cooperative_groups.h>
+#include <cuda.h>
 #include <cstddef>
 
 #include "kda_glr_math.cuh"
 #include "kda_ops_internal.h"
+#include "kda_sm100.cuh"
 
 namespace kda {
 namespace {
@@ -37,9 +39,14 @@ constexpr int kTile = kGlrBlock;  // tokens of a tile
 constexpr int kRow = 128;         // elements of a tile row in shared memory
 constexpr int kMaxCluster = 8;
 
-// How a row of d channels is accessed: four channels per lane at once; or element by element, the
-// copies to shared memory then in words of 4 bytes where rows start on one, else through registers.
-enum Access { kVec4 = 0, kWord = 1, kElem = 2 };
+// How rows of d channels come to shared memory: by tensor copies where rows start on 16 bytes; else
+// four channels per lane at once, in words of 4 bytes, or element by element through registers.
+enum Access { kTensor = 0, kVec4 = 1, kWord = 2, kElem = 3 };
+constexpr uint64_t kWaitNs = 1000000000ull;  // limit of a wait for a copy or for another warp
+
+struct Maps {
+  CUtensorMap x, raw, out;
+};
 
 template <int kBytes>
 __device__ __forceinline__ void cp_async(void* dst, const void* src) {
@@ -58,7 +65,7 @@ __device__ __forceinline__ void cp_async_wait() {
 // One row of d channels to shared memory, by the warp that will read it.
 template <typename T>
 __device__ __forceinline__ void copy_row(T* dst, const T* src, int d, int lane, Access how) {
-  if (how == kVec4) {
+  if (how <= kVec4) {
     if (4 * lane < d) cp_async<4 * sizeof(T)>(dst + 4 * lane, src + 4 * lane);
   } else if (how == kWord) {
     constexpr int kPer = 4 / sizeof(T);
@@ -111,27 +118,50 @@ __device__ __forceinline__ bool sequence(const int32_t* cu, int b, int64_t T, in
   return s0 >= 0 && n >= 0 && (int64_t)s0 + n <= T;
 }
 
+// A pair to the same place in the shared memory of CTA `rank` of the cluster, counted on that CTA's
+// barrier.  The message orders itself: a cluster barrier would make every thread wait until its
+// outputs have been written to global memory.
+__device__ __forceinline__ void send_map(float2* to, uint64_t* bar, int rank, float a, float b) {
+  uint32_t dst, rbar;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(sm100::smem_addr(to)), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rbar) : "r"(sm100::smem_addr(bar)), "r"(rank));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(dst),
+               "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(rbar)
+               : "memory");
+}
 // ------------------------------------------------------------------------------------ forward
+//
+// 16 warps compute, 4 tokens of a 64-token tile each; 4 warps carry: a thread per channel, which folds
+// the tokens' maps, trades the tile's map with the other CTAs and hands every warp the state that enters
+// its tokens; one of its threads brings in the tiles, a tensor copy per input (256-byte copies of single
+// rows took the issuing warps about 50 cycles each).  The computing warps never wait for a
+// carry of their own step: they work out the gates and maps of the next tile first, and only then
+// finish the last one, whose a and b they have kept in registers.
 
-constexpr int kFwdThreads = 256;
-constexpr int kFwdWarps = kFwdThreads / 32;
+constexpr int kFwdWarps = 16;
 constexpr int kFwdRows = kTile / kFwdWarps;  // consecutive tokens of a warp
+constexpr int kCarryWarps = kRow / 32;
+constexpr int kFwdThreads = 32 * (kFwdWarps + kCarryWarps);
 
-template <typename TX, typename TR>
+template <typename TX, typename TR, typename TO>
 struct FwdSmem {
-  static constexpr int kStages = 2;
+  static constexpr int kStages = sizeof(TX) + sizeof(TR) <= 4 ? 4 : sizeof(TX) + sizeof(TR) <= 6 ? 3 : 2;
   static constexpr int kMaxRanks = kMaxCluster;
-  TX x[kStages][kTile][kRow];
-  TR raw[kStages][kTile][kRow];
-  float beta[kStages][kTile];
-  MapRow warp_map[kFwdWarps];
-  MapRow tile_map[2][kMaxRanks];  // every other step's: a CTA may be one step ahead of another
+  alignas(128) TX x[kStages][kTile * kRow];
+  alignas(128) TR raw[kStages][kTile * kRow];
+  alignas(128) TO out[kTile * kRow];
+  float2 map[2][kFwdWarps][kRow];       // (A, B) of a warp's tokens; A then becomes the entering state
+  float2 tile_map[2][kMaxRanks][kRow];  // of a step's tiles
+  uint64_t full[kStages];               // a tile has arrived
+  uint64_t mapped[2], entered[2];       // the warps' maps are there; the states entering them are
+  uint64_t tiles_in[2];                 // the tiles' maps have arrived
 };
 
-template <typename TX, typename TR, bool kNorm>
-__global__ void __launch_bounds__(kFwdThreads, 2) glr_fwd_kernel(const GlrArgs p, const Access how, const bool vec_out) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  using Smem = FwdSmem<TX, TR>;
+template <typename TX, typename TR, typename TO, bool kNorm, bool kSafe>
+__global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p, const __grid_constant__ Maps maps,
+                                                                 const Access how, const bool out_map, const bool vec_out) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  using Smem = FwdSmem<TX, TR, TO>;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   constexpr int kStages = Smem::kStages;
 
@@ -147,122 +177,220 @@ __global__ void __launch_bounds__(kFwdThreads, 2) glr_fwd_kernel(const GlrArgs p
     return;
   }
   if (n == 0) return;
-  float* state = p.pool + ((size_t)slot * p.H + h) * d;
-  const HeadGate gate = head_gate(p.a_log[h], p.flags & KDA_GATE_SAFE, p.lb);
-  const bool prob = p.flags & KDA_BETA_PROB;
-  float2 bias0, bias1, c0, c1;  // the bias, and the state entering the cluster's next tiles
-  load4(p.dt_bias + (size_t)h * d, d, lane, bias0, bias1);
-  load4(state, d, lane, c0, c1);
-
   const size_t row = (size_t)p.H * d;  // elements from a token to the next
   const size_t first = (size_t)s0 * row + (size_t)h * d;
-  const TX* x = reinterpret_cast<const TX*>(p.x) + first;
-  const TR* raw = reinterpret_cast<const TR*>(p.raw_gate) + first;
-  const float* beta = p.beta + (size_t)s0 * p.H + h;
   const int tiles = (n + kTile - 1) / kTile, steps = (tiles + ranks - 1) / ranks;
 
-  auto fetch = [&](int step) {  // this warp's tokens of tile step * ranks + rank
-    const int stage = step % kStages, t0 = (step * ranks + rank) * kTile + warp * kFwdRows;
-#pragma unroll
-    for (int r = 0; r < kFwdRows; ++r) {
-      if (step < steps && t0 + r < n) {
-        copy_row(sm.x[stage][warp * kFwdRows + r], x + (t0 + r) * row, d, lane, how);
-        copy_row(sm.raw[stage][warp * kFwdRows + r], raw + (t0 + r) * row, d, lane, how);
-      }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) sm100::mbar_init(sm100::smem_addr(&sm.full[s]), 1);
+    for (int s = 0; s < 2; ++s) {
+      sm100::mbar_init(sm100::smem_addr(&sm.mapped[s]), kFwdWarps);
+      sm100::mbar_init(sm100::smem_addr(&sm.entered[s]), kCarryWarps);
+      sm100::mbar_init(sm100::smem_addr(&sm.tiles_in[s]), 1);
     }
-    if (lane < kFwdRows && step < steps && t0 + lane < n)
-      cp_async<4>(&sm.beta[stage][warp * kFwdRows + lane], beta + (size_t)(t0 + lane) * p.H);
+    sm100::fence_mbar_init();
+  }
+  cluster.sync();
+  auto wait = [&](uint64_t* bar, int parity) {
+    if (!sm100::mbar_wait_sleep(sm100::smem_addr(bar), parity & 1, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+  };
+
+  const int pitch = how == kTensor ? d : kRow;  // elements of a tile's row
+
+  if (warp >= kFwdWarps) {
+    // ---------------------------------------------------------------- carrying warps
+    const int c = threadIdx.x - 32 * kFwdWarps;
+    auto fetch = [&](int step) {
+      if (how != kTensor || c != 0 || step >= steps) return;
+      const int stage = step % kStages, tile = step * ranks + rank, t = s0 + tile * kTile;
+      const uint32_t bar = sm100::smem_addr(&sm.full[stage]);
+      if (tile >= tiles) return sm100::mbar_arrive(bar);  // nothing there: whatever is left in the rows will do
+      sm100::mbar_arrive_expect_tx(bar, kTile * d * (uint32_t)(sizeof(TX) + sizeof(TR)));
+      sm100::tma_load_3d(sm100::smem_addr(sm.x[stage]), &maps.x, 0, h, t, bar);
+      sm100::tma_load_3d(sm100::smem_addr(sm.raw[stage]), &maps.raw, 0, h, t, bar);
+    };
+    for (int s = 0; s < kStages; ++s) fetch(s);
+    float* state = p.pool + ((size_t)slot * p.H + h) * d;
+    float carry = c < d ? state[c] : 0.f;
+    for (int step = 0; step < steps; ++step) {
+      const int par = step & 1;
+      wait(&sm.mapped[par], step >> 1);
+      float2 of[kFwdWarps];
+      float pa = 1.f, pb = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFwdWarps; ++w) of[w] = sm.map[par][w][c];
+#pragma unroll
+      for (int w = 0; w < kFwdWarps; ++w) {
+        pb = fmaf(pb, of[w].x, of[w].y);
+        pa *= of[w].x;
+      }
+      for (int k = 0; k < ranks; ++k) send_map(&sm.tile_map[par][rank][c], &sm.tiles_in[par], k, pa, pb);
+      if (c == 0)
+        sm100::mbar_arrive_expect_tx(sm100::smem_addr(&sm.tiles_in[par]), ranks * kRow * (uint32_t)sizeof(float2));
+      fetch(step + kStages);  // into the tile that has just been read
+      wait(&sm.tiles_in[par], step >> 1);
+      float in = carry;
+      float2 m[kMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) m[k] = k < ranks ? sm.tile_map[par][k][c] : make_float2(1.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        if (k == rank) in = carry;
+        carry = fmaf(carry, m[k].x, m[k].y);
+      }
+      const int tile = step * ranks + rank;
+      if (p.checkpoints && c < d && tile < tiles)
+        p.checkpoints[((size_t)(s0 / kTile + b + tile) * p.H + h) * d + c] = in;
+#pragma unroll
+      for (int w = 0; w < kFwdWarps; ++w) {
+        sm.map[par][w][c].x = in;
+        in = fmaf(in, of[w].x, of[w].y);
+      }
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(sm100::smem_addr(&sm.entered[par]));
+    }
+    if (rank == 0 && c < d) state[c] = carry;
+    return;
+  }
+
+  // ------------------------------------------------------------------ computing warps
+  const HeadGate gate = head_gate(p.a_log[h], kSafe, p.lb);
+  const bool prob = p.flags & KDA_BETA_PROB;
+  float2 bias0, bias1;
+  load4(p.dt_bias + (size_t)h * d, d, lane, bias0, bias1);
+  bias0 = mul2(bias0, both(kLog2e));
+  bias1 = mul2(bias1, both(kLog2e));
+  const int row0 = warp * kFwdRows, own = row0 + (lane & (kFwdRows - 1));
+  const float* beta = p.beta + (size_t)s0 * p.H + h;
+  TO* out = reinterpret_cast<TO*>(p.out) + first + (size_t)row0 * row;
+  // beta of one of the warp's tokens per lane, a step ahead
+  auto load_beta = [&](int step) {
+    const int t = (step * ranks + rank) * kTile + own;
+    return step < steps && t < n ? beta[(size_t)t * p.H] : 0.f;
+  };
+  float bt = beta_fast(load_beta(0), prob), next_beta = load_beta(1);
+
+  auto copy = [&](int step) {  // without tensor copies, the warp's own rows of a step's tile
+    const int t0 = (step * ranks + rank) * kTile + row0, rows = step < steps ? min(max(n - t0, 0), kFwdRows) : 0;
+    const size_t at = first + (size_t)t0 * row;
+    for (int r = 0; r < rows; ++r) {
+      const int to = (row0 + r) * kRow;
+      copy_row(sm.x[step % kStages] + to, reinterpret_cast<const TX*>(p.x) + at + r * row, d, lane, how);
+      copy_row(sm.raw[step % kStages] + to, reinterpret_cast<const TR*>(p.raw_gate) + at + r * row, d, lane, how);
+    }
     cp_async_commit();
   };
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(s);
+  if (how != kTensor)
+    for (int s = 0; s < kStages - 1; ++s) copy(s);
 
-  for (int step = 0; step < steps; ++step) {
-    __syncwarp();  // the stage that is filled next has been read
-    fetch(step + kStages - 1);
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
-    const int stage = step % kStages, par = step & 1;
-    const int tile = step * ranks + rank, t0 = tile * kTile + warp * kFwdRows;
-
-    // ---- this warp's tokens: a and b = beta s x of every token, and their map
-    float bt = 0.f;
-    if (lane < kFwdRows) bt = beta_f32(sm.beta[stage][warp * kFwdRows + lane], prob);
+  struct Kept {  // a and b = beta s x of the warp's tokens
     float2 a0[kFwdRows], a1[kFwdRows], b0[kFwdRows], b1[kFwdRows];
-    Map4 mine{both(1.f), both(1.f), both(0.f), both(0.f)};
+  };
+  auto work_out = [&](int step, Kept& k) {
+    const int stage = step % kStages, par = step & 1;
+    if (how == kTensor) {
+      wait(&sm.full[stage], step / kStages);
+    } else {
+      __syncwarp();  // the rows that are replaced next have been read
+      copy(step + kStages - 1);
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+    }
+    const TR* raws = sm.raw[stage] + row0 * pitch + 4 * lane;
+    const TX* xs = sm.x[stage] + row0 * pitch + 4 * lane;
 #pragma unroll
     for (int r = 0; r < kFwdRows; ++r) {
       const float bt_r = __shfl_sync(0xffffffffu, bt, r);
-      a0[r] = a1[r] = both(1.f);
-      b0[r] = b1[r] = both(0.f);
-      if (t0 + r < n) {
-        float2 z0, z1, x0, x1;
-        unpack4(&sm.raw[stage][warp * kFwdRows + r][4 * lane], z0, z1);
-        unpack4(&sm.x[stage][warp * kFwdRows + r][4 * lane], x0, x1);
-        z0 = add2(z0, bias0);
-        z1 = add2(z1, bias1);
-        const float2 g0 = clamp2(gate_log2(z0, exp_neg_abs(z0), gate.c2), gate.lb2);
-        const float2 g1 = clamp2(gate_log2(z1, exp_neg_abs(z1), gate.c2), gate.lb2);
-        a0[r] = make_float2(ex2(g0.x), ex2(g0.y));
-        a1[r] = make_float2(ex2(g1.x), ex2(g1.y));
-        b0[r] = mul2(x0, both(bt_r));
-        b1[r] = mul2(x1, both(bt_r));
-        if constexpr (kNorm) {
-          float2 inv, root;
-          roots(one_minus_sq(g0, a0[r]), inv, root);
-          b0[r] = mul2(b0[r], root);
-          roots(one_minus_sq(g1, a1[r]), inv, root);
-          b1[r] = mul2(b1[r], root);
-        }
-        mine.a0 = mul2(mine.a0, a0[r]);
-        mine.a1 = mul2(mine.a1, a1[r]);
-        mine.b0 = fma2(mine.b0, a0[r], b0[r]);
-        mine.b1 = fma2(mine.b1, a1[r], b1[r]);
+      float2 z0, z1, x0, x1;
+      unpack4(raws + r * pitch, z0, z1);
+      unpack4(xs + r * pitch, x0, x1);
+      z0 = pre_log2(z0, bias0);
+      z1 = pre_log2(z1, bias1);
+      float2 g0 = gate_log2(z0, exp_neg_abs(z0), gate.c), g1 = gate_log2(z1, exp_neg_abs(z1), gate.c);
+      if constexpr (kSafe) {
+        g0 = clamp2(g0, gate.lb2);
+        g1 = clamp2(g1, gate.lb2);
+      }
+      k.a0[r] = make_float2(ex2(g0.x), ex2(g0.y));
+      k.a1[r] = make_float2(ex2(g1.x), ex2(g1.y));
+      k.b0[r] = mul2(x0, both(bt_r));
+      k.b1[r] = mul2(x1, both(bt_r));
+      if constexpr (kNorm) {
+        const float2 u0 = one_minus_sq(g0, k.a0[r]), u1 = one_minus_sq(g1, k.a1[r]);
+        k.b0[r] = mul2(k.b0[r], mul2(u0, rsq2(u0)));
+        k.b1[r] = mul2(k.b1[r], mul2(u1, rsq2(u1)));
       }
     }
-    write_map(sm.warp_map[warp], lane, mine);
-    __syncthreads();
-
-    // ---- maps of the warps before this one; the last warp has the tile's and hands it around
-    Map4 before{both(1.f), both(1.f), both(0.f), both(0.f)};
-    auto fold = [&](Map4& f, const Map4& m) {
-      f.a0 = mul2(f.a0, m.a0);
-      f.a1 = mul2(f.a1, m.a1);
-      f.b0 = fma2(f.b0, m.a0, m.b0);
-      f.b1 = fma2(f.b1, m.a1, m.b1);
-    };
-    for (int w = 0; w < warp; ++w) fold(before, read_map(sm.warp_map[w], lane));
-    if (warp == kFwdWarps - 1) {
-      Map4 all = before;
-      fold(all, mine);
-      for (int k = 0; k < ranks; ++k) write_map(*cluster.map_shared_rank(&sm.tile_map[par][rank], k), lane, all);
-    }
-    cluster.sync();
-    float2 in0 = c0, in1 = c1;  // the state entering this tile, and then the next step's tiles
-    for (int k = 0; k < ranks; ++k) {
-      if (k == rank) in0 = c0, in1 = c1;
-      const Map4 m = read_map(sm.tile_map[par][k], lane);
-      c0 = fma2(c0, m.a0, m.b0);
-      c1 = fma2(c1, m.a1, m.b1);
-    }
-    if (t0 < n) {
-      if (warp == 0 && p.checkpoints)
-        put4(p.checkpoints + ((size_t)(s0 / kTile + b + tile) * p.H + h) * d, d, lane, in0, in1, false);
-      in0 = fma2(before.a0, in0, before.b0);
-      in1 = fma2(before.a1, in1, before.b1);
+    const int left = n - (step * ranks + rank) * kTile - row0;
+    if (left < kFwdRows) {  // rows past the end, whatever they hold, are the identity
 #pragma unroll
       for (int r = 0; r < kFwdRows; ++r) {
-        in0 = fma2(a0[r], in0, b0[r]);
-        in1 = fma2(a1[r], in1, b1[r]);
-        if (t0 + r < n) {
-          const size_t at = first + (size_t)(t0 + r) * row;
-          if (p.out_bf16) put4(reinterpret_cast<__nv_bfloat16*>(p.out) + at, d, lane, in0, in1, vec_out);
-          else put4(reinterpret_cast<float*>(p.out) + at, d, lane, in0, in1, vec_out);
+        if (r >= left) {
+          k.a0[r] = k.a1[r] = both(1.f);
+          k.b0[r] = k.b1[r] = both(0.f);
         }
       }
     }
+    Map4 m{k.a0[0], k.a1[0], k.b0[0], k.b1[0]};
+#pragma unroll
+    for (int r = 1; r < kFwdRows; ++r) {
+      m.a0 = mul2(m.a0, k.a0[r]);
+      m.a1 = mul2(m.a1, k.a1[r]);
+      m.b0 = fma2(m.b0, k.a0[r], k.b0[r]);
+      m.b1 = fma2(m.b1, k.a1[r], k.b1[r]);
+    }
+    float4* to = reinterpret_cast<float4*>(&sm.map[par][warp][4 * lane]);
+    to[0] = make_float4(m.a0.x, m.b0.x, m.a0.y, m.b0.y);
+    to[1] = make_float4(m.a1.x, m.b1.x, m.a1.y, m.b1.y);
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(sm100::smem_addr(&sm.mapped[par]));
+    bt = beta_fast(next_beta, prob);
+    next_beta = load_beta(step + 2);
+  };
+  // outputs leave through shared memory, a tensor copy per warp: plain stores of all warps at the same
+  // point of the step held them up for a third of it
+  TO* staged = sm.out + row0 * kRow;
+  auto finish = [&](int step, const Kept& k) {
+    const int par = step & 1, tile = step * ranks + rank, left = n - tile * kTile - row0;
+    wait(&sm.entered[par], step >> 1);
+    const float4* from = reinterpret_cast<const float4*>(&sm.map[par][warp][4 * lane]);
+    const float4 lo = from[0], hi = from[1];
+    float2 in0 = make_float2(lo.x, lo.z), in1 = make_float2(hi.x, hi.z);
+    const bool copied = out_map && left >= kFwdRows;
+    if (copied) {
+      sm100::bulk_wait_read_all();  // (the issuing lane's) the rows have left
+      __syncwarp();
+    }
+    TO* to = out + (size_t)tile * kTile * row;
+#pragma unroll
+    for (int r = 0; r < kFwdRows; ++r, to += row) {
+      in0 = fma2(k.a0[r], in0, k.b0[r]);
+      in1 = fma2(k.a1[r], in1, k.b1[r]);
+      if (copied) {
+        if (4 * lane < d) store4(staged + r * d + 4 * lane, in0, in1);
+      } else if (r < left) {
+        put4(to, d, lane, in0, in1, vec_out);
+      }
+    }
+    if (copied) {
+      sm100::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        sm100::tma_store_3d(&maps.out, sm100::smem_addr(staged), 0, h, s0 + tile * kTile + row0);
+        sm100::bulk_commit();
+      }
+    }
+  };
+  Kept even, odd;
+  work_out(0, even);
+  for (int step = 0; step < steps; step += 2) {
+    if (step + 1 < steps) work_out(step + 1, odd);
+    finish(step, even);
+    if (step + 1 >= steps) break;
+    if (step + 2 < steps) work_out(step + 2, even);
+    finish(step + 1, odd);
   }
-  if (rank == 0 && warp == 0) put4(state, d, lane, c0, c1, false);
+  sm100::bulk_wait_all();
 }
 
 // ------------------------------------------------------------------------------------ backward
@@ -287,7 +415,7 @@ struct BwdSmem {
 template <typename TX, typename TR, typename TO, bool kNorm>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     glr_bwd_kernel(const GlrBwdArgs p, const Access how, const bool vec_grad) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   using Smem = BwdSmem<TX, TR, TO>;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   constexpr int kStages = Smem::kStages;
@@ -313,10 +441,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
   const float a_log = p.a_log[h];
   const HeadGate gate = head_gate(a_log, p.flags & KDA_GATE_SAFE, p.lb);
-  const float minus_c = gate.c2 * kLn2;  // -exp(a_log)
   const bool prob = p.flags & KDA_BETA_PROB;
   float2 bias0, bias1, c0 = both(0.f), c1 = both(0.f);  // c: a D of the token after the cluster's tiles
   load4(p.dt_bias + (size_t)h * d, d, lane, bias0, bias1);
+  bias0 = mul2(bias0, both(kLog2e));
+  bias1 = mul2(bias1, both(kLog2e));
   if (p.d_final) load4(p.d_final + ((size_t)b * p.H + h) * d, d, lane, c0, c1);
 
   const size_t row = (size_t)p.H * d;
@@ -384,20 +513,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         float2 z0, z1, x0, x1;
         unpack4(&sm.raw[stage][warp * kBwdRows + r][4 * lane], z0, z1);
         unpack4(&sm.x[stage][warp * kBwdRows + r][4 * lane], x0, x1);
-        z0 = add2(z0, bias0);
-        z1 = add2(z1, bias1);
-        g0[r] = gate_log2(z0, exp_neg_abs(z0), gate.c2);
-        g1[r] = gate_log2(z1, exp_neg_abs(z1), gate.c2);
+        z0 = pre_log2(z0, bias0);
+        z1 = pre_log2(z1, bias1);
+        g0[r] = gate_log2(z0, exp_neg_abs(z0), gate.c);
+        g1[r] = gate_log2(z1, exp_neg_abs(z1), gate.c);
         const float2 cg0 = clamp2(g0[r], gate.lb2), cg1 = clamp2(g1[r], gate.lb2);
         a0[r] = make_float2(ex2(cg0.x), ex2(cg0.y));
         a1[r] = make_float2(ex2(cg1.x), ex2(cg1.y));
         b0[r] = mul2(x0, both(bt_r));
         b1[r] = mul2(x1, both(bt_r));
         if constexpr (kNorm) {
-          float2 inv;
-          roots(one_minus_sq(cg0, a0[r]), inv, q0[r]);
+          const float2 u0 = one_minus_sq(cg0, a0[r]), u1 = one_minus_sq(cg1, a1[r]);
+          q0[r] = mul2(u0, rsq2(u0));
+          q1[r] = mul2(u1, rsq2(u1));
           b0[r] = mul2(b0[r], q0[r]);
-          roots(one_minus_sq(cg1, a1[r]), inv, q1[r]);
           b1[r] = mul2(b1[r], q1[r]);
         }
         mine.a0 = mul2(mine.a0, a0[r]);
@@ -482,9 +611,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       float2 xs0 = mul2(D0, x0), xs1 = mul2(D1, x1);              // D x, times s for dbeta
       float2 dx0 = mul2(D0, both(bt_r)), dx1 = mul2(D1, both(bt_r));
       if constexpr (kNorm) {
-        // ds/dg = -a^2 / s (0 where s is: nothing is let in)
-        auto slope = [](float2 a, float2 s) {
-          return make_float2(s.x > 0.f ? __fdividef(-a.x * a.x, s.x) : 0.f, s.y > 0.f ? __fdividef(-a.y * a.y, s.y) : 0.f);
+        auto slope = [](float2 a, float2 s) {  // ds/dg = -a^2 / s
+          return make_float2(__fdividef(-a.x * a.x, s.x), __fdividef(-a.y * a.y, s.y));
         };
         dg0 = fma2(mul2(xs0, both(bt_r)), slope(a0[r], q0[r]), dg0);
         dg1 = fma2(mul2(xs1, both(bt_r)), slope(a1[r], q1[r]), dg1);
@@ -500,14 +628,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float2 lim = both(-3.0e38f);
       sum_log = fma2(dg0, make_float2(fmaxf(g0[r].x, lim.x), fmaxf(g0[r].y, lim.y)), sum_log);
       sum_log = fma2(dg1, make_float2(fmaxf(g1[r].x, lim.x), fmaxf(g1[r].y, lim.y)), sum_log);
-      z0 = add2(z0, bias0);
-      z1 = add2(z1, bias1);
-      auto sigmoid = [](float z) {  // e / (1 + e) or 1 / (1 + e) with e = exp(-|z|)
-        const float e = ex2(-fabsf(z) * kLog2e);
+      z0 = pre_log2(z0, bias0);
+      z1 = pre_log2(z1, bias1);
+      auto sigmoid = [](float z) {  // e / (1 + e) or 1 / (1 + e) with e = exp(-|z|), z being in units of log2
+        const float e = ex2(-fabsf(z));
         return (z >= 0.f ? 1.f : e) * rcp(1.f + e);
       };
-      const float2 dr0 = mul2(mul2(dg0, both(minus_c)), make_float2(sigmoid(z0.x), sigmoid(z0.y)));
-      const float2 dr1 = mul2(mul2(dg1, both(minus_c)), make_float2(sigmoid(z1.x), sigmoid(z1.y)));
+      const float2 dr0 = mul2(mul2(dg0, both(gate.c)), make_float2(sigmoid(z0.x), sigmoid(z0.y)));
+      const float2 dr1 = mul2(mul2(dg1, both(gate.c)), make_float2(sigmoid(z1.x), sigmoid(z1.y)));
       sum_bias0 = add2(sum_bias0, dr0);
       sum_bias1 = add2(sum_bias1, dr1);
       const int c = 4 * lane;
@@ -602,19 +730,18 @@ __global__ void __launch_bounds__(kDecThreads) glr_decode_kernel(const GlrArgs p
   const HeadGate gate = head_gate(p.a_log[h], p.flags & KDA_GATE_SAFE, p.lb);
   const float bt = beta_f32(p.beta[bh], p.flags & KDA_BETA_PROB);
   auto step = [&](float2 s, float2 xv, float2 z) {
-    const float2 g = clamp2(gate_log2(z, exp_neg_abs(z), gate.c2), gate.lb2);
+    const float2 g = clamp2(gate_log2(z, exp_neg_abs(z), gate.c), gate.lb2);
     const float2 a = make_float2(ex2(g.x), ex2(g.y));
     float2 in = mul2(xv, both(bt));
     if (p.flags & KDA_INPUT_NORM) {
-      float2 inv, root;
-      roots(one_minus_sq(g, a), inv, root);
-      in = mul2(in, root);
+      const float2 u = one_minus_sq(g, a);
+      in = mul2(in, mul2(u, rsq2(u)));
     }
     return fma2(a, s, in);
   };
-  s0 = step(s0, x0, add2(z0, v0));
+  s0 = step(s0, x0, pre_log2(z0, mul2(v0, both(kLog2e))));
   if constexpr (kPer == 4) {
-    s1 = step(s1, x1, add2(z1, v1));
+    s1 = step(s1, x1, pre_log2(z1, mul2(v1, both(kLog2e))));
     store4(state, s0, s1);
     if (p.out_bf16) store4(reinterpret_cast<__nv_bfloat16*>(p.out) + i, s0, s1);
     else store4(reinterpret_cast<float*>(p.out) + i, s0, s1);
@@ -633,7 +760,7 @@ int cluster_size(int32_t batch, int64_t T, int32_t H, int most) {
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t tiles = (T / batch + kTile - 1) / kTile;
   int c = 1;
-  while (c < most && (int64_t)batch * H * c < 2 * sms && 2 * c <= tiles) c *= 2;
+  while (c < most && (int64_t)batch * H * c * 8 < 6 * sms && 2 * c <= tiles) c *= 2;
   return c;
 }
 
@@ -659,22 +786,53 @@ cudaError_t launch_cluster(Kernel kernel, unsigned grid, int threads, size_t sme
 // how rows of d elements of the given tensors can be copied to shared memory
 template <typename T>
 Access access_of(const void* p, int d) {
+  if (d * sizeof(T) % 16 == 0 && aligned(p, 16)) return kTensor;
   if (d % 4 == 0 && aligned(p, 4 * sizeof(T))) return kVec4;
   return (d * sizeof(T)) % 4 == 0 && aligned(p, 4) ? kWord : kElem;
 }
 Access worse(Access a, Access b) { return a > b ? a : b; }
 
-template <typename TX, typename TR>
+// [tokens][heads][d] in boxes of one head of so many tokens
+template <typename T>
+bool encode(CUtensorMap* m, const void* base, int64_t tokens, int heads, int d, int rows = kTile) {
+  using Fn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                          const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                          CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Fn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<Fn>(p)
+               : nullptr;
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * sizeof(T), (cuuint64_t)heads * d * sizeof(T)};
+  const cuuint32_t box[3] = {(cuuint32_t)d, 1, (cuuint32_t)rows}, each[3] = {1, 1, 1};
+  return fn(m, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+            const_cast<void*>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename TX, typename TR, typename TO>
 cudaError_t fwd(const GlrArgs& a, cudaStream_t stream) {
-  const Access how = worse(access_of<TX>(a.x, a.d), access_of<TR>(a.raw_gate, a.d));
-  const bool vec_out = a.d % 4 == 0 && aligned(a.out, a.out_bf16 ? 8 : 16);
-  const int ranks = cluster_size(a.batch, a.total_tokens, a.H, FwdSmem<TX, TR>::kMaxRanks);
+  Access how = worse(access_of<TX>(a.x, a.d), access_of<TR>(a.raw_gate, a.d));
+  Maps maps{};
+  if (how == kTensor && (a.total_tokens == 0 || !encode<TX>(&maps.x, a.x, a.total_tokens, a.H, a.d) ||
+                         !encode<TR>(&maps.raw, a.raw_gate, a.total_tokens, a.H, a.d)))
+    how = kVec4;
+  const bool out_map = access_of<TO>(a.out, a.d) == kTensor && a.total_tokens > 0 &&
+                       encode<TO>(&maps.out, a.out, a.total_tokens, a.H, a.d, kFwdRows);
+  const bool vec_out = a.d % 4 == 0 && aligned(a.out, 4 * sizeof(TO));
+  const int ranks = cluster_size(a.batch, a.total_tokens, a.H, FwdSmem<TX, TR, TO>::kMaxRanks);
   const int64_t grid = (int64_t)a.batch * a.H * ranks;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  const size_t smem = sizeof(FwdSmem<TX, TR>);
-  if (a.flags & KDA_INPUT_NORM)
-    return launch_cluster(glr_fwd_kernel<TX, TR, true>, (unsigned)grid, kFwdThreads, smem, ranks, stream, a, how, vec_out);
-  return launch_cluster(glr_fwd_kernel<TX, TR, false>, (unsigned)grid, kFwdThreads, smem, ranks, stream, a, how, vec_out);
+  const size_t smem = sizeof(FwdSmem<TX, TR, TO>);
+  const bool norm = a.flags & KDA_INPUT_NORM, safe = a.flags & KDA_GATE_SAFE;
+  const auto kernel = norm ? (safe ? glr_fwd_kernel<TX, TR, TO, true, true> : glr_fwd_kernel<TX, TR, TO, true, false>)
+                           : (safe ? glr_fwd_kernel<TX, TR, TO, false, true> : glr_fwd_kernel<TX, TR, TO, false, false>);
+  return launch_cluster(kernel, (unsigned)grid, kFwdThreads, smem, ranks, stream, a, maps, how, out_map, vec_out);
 }
 
 template <typename TX, typename TR, typename TO>
@@ -713,8 +871,10 @@ int glr_bwd_partials(int32_t batch, int64_t total_tokens, int32_t H) {
 }
 
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t stream) {
-  if (!a.x_bf16) return fwd<float, float>(a, stream);
-  return a.raw_bf16 ? fwd<__nv_bfloat16, __nv_bfloat16>(a, stream) : fwd<__nv_bfloat16, float>(a, stream);
+  using bf16 = __nv_bfloat16;
+  if (!a.x_bf16) return fwd<float, float, float>(a, stream);
+  if (a.raw_bf16) return a.out_bf16 ? fwd<bf16, bf16, bf16>(a, stream) : fwd<bf16, bf16, float>(a, stream);
+  return a.out_bf16 ? fwd<bf16, float, bf16>(a, stream) : fwd<bf16, float, float>(a, stream);
 }
 
 cudaError_t launch_glr_bwd(const GlrBwdArgs& a, cudaStream_t stream) {

@@ -3,7 +3,7 @@
 // The forward pass at HBM speed has about 13 issue slots and 6 MUFU cycles per element and SM
 // sub-core to spend, so the gate is evaluated two channels at a time (fma.rn.f32x2 and friends)
 // with two MUFU operations per element: e = 2^(-|z| log2 e) and a = 2^(g log2 e).  softplus(z) =
-// max(z, 0) + log1p(e) takes log1p as e times a degree-9 polynomial: a logarithm of the rounded
+// max(z, 0) + log1p(e) takes log1p as e times a degree-7 polynomial: a logarithm of the rounded
 // 1 + e would lose the gates of slow channels (softplus << 1), whose decays multiply up over
 // thousands of tokens.
 //
@@ -63,68 +63,60 @@ __device__ __forceinline__ float rsq(float x) {
   return r;
 }
 
-// log1p(e) / e for e in [0, 1] (relative error 1.2e-7)
-__device__ __forceinline__ float2 log1p_ratio(float2 e) {
-  float2 p = both(-0.0032439807f);
-  p = fma2(p, e, both(0.0198512617f));
-  p = fma2(p, e, both(-0.0569591597f));
-  p = fma2(p, e, both(0.106036171f));
-  p = fma2(p, e, both(-0.153055698f));
-  p = fma2(p, e, both(0.196759313f));
-  p = fma2(p, e, both(-0.249541327f));
-  p = fma2(p, e, both(0.333299637f));
-  p = fma2(p, e, both(-0.499999017f));
-  return fma2(p, e, both(1.f));
+// log2(1 + e) / e for e in [0, 1] (relative error 3.2e-7, about that of the hardware exponential)
+__device__ __forceinline__ float2 log2_1p_ratio(float2 e) {
+  float2 p = both(-0.0123193823f);
+  p = fma2(p, e, both(0.0636075735f));
+  p = fma2(p, e, both(-0.15535143f));
+  p = fma2(p, e, both(0.25600943f));
+  p = fma2(p, e, both(-0.353394717f));
+  p = fma2(p, e, both(0.480063677f));
+  p = fma2(p, e, both(-0.721310079f));
+  return fma2(p, e, both(1.44269478f));
 }
 
-// expm1(y) / y for y in [-1/2, 0] (relative error 5.4e-8)
-__device__ __forceinline__ float2 expm1_ratio(float2 y) {
-  float2 p = both(0.00112163462f);
-  p = fma2(p, y, both(0.00818738528f));
-  p = fma2(p, y, both(0.0416290872f));
-  p = fma2(p, y, both(0.166662246f));
-  p = fma2(p, y, both(0.499999821f));
-  return fma2(p, y, both(1.f));
+// (1 - exp(-t)) / t for t in [0, 1/2] (relative error 1.5e-7)
+__device__ __forceinline__ float2 one_minus_exp_ratio(float2 t) {
+  float2 p = both(0.00677103736f);
+  p = fma2(p, t, both(-0.0410012789f));
+  p = fma2(p, t, both(0.166548148f));
+  p = fma2(p, t, both(-0.49999249f));
+  return fma2(p, t, both(0.99999994f));
 }
 
-// What one head's gate needs besides the pre-activation: -exp(a_log) log2 e, and the safe gate's
-// bound times log2 e (-inf when there is none).
+// What one head's gate needs besides the pre-activation: -exp(a_log), and the safe gate's bound times
+// log2 e (-inf when there is none).
 struct HeadGate {
-  float c2, lb2;
+  float c, lb2;
 };
 __device__ __forceinline__ HeadGate head_gate(float a_log, bool safe, float lb) {
-  return {-expf(a_log) * kLog2e, safe ? lb * kLog2e : -INFINITY};
+  return {-expf(a_log), safe ? lb * kLog2e : -INFINITY};
 }
 
-// e = exp(-|z|)
-__device__ __forceinline__ float2 exp_neg_abs(float2 z) {
-  return make_float2(ex2(-fabsf(z.x) * kLog2e), ex2(-fabsf(z.y) * kLog2e));
-}
-// g log2 e before the clamp, from z and e
-__device__ __forceinline__ float2 gate_log2(float2 z, float2 e, float c2) {
-  const float2 sp = fma2(e, log1p_ratio(e), make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
-  return mul2(both(c2), sp);
+// The gate is kept in units of log2: z2 = z log2 e from the raw value and the bias times log2 e, then
+// e = exp(-|z|), then g log2 e = -exp(a_log) (max(z2, 0) + log2(1 + e)) before any clamp.
+__device__ __forceinline__ float2 pre_log2(float2 raw, float2 bias2) { return fma2(raw, both(kLog2e), bias2); }
+__device__ __forceinline__ float2 exp_neg_abs(float2 z2) { return make_float2(ex2(-fabsf(z2.x)), ex2(-fabsf(z2.y))); }
+__device__ __forceinline__ float2 gate_log2(float2 z2, float2 e, float c) {
+  return mul2(both(c), fma2(e, log2_1p_ratio(e), make_float2(fmaxf(z2.x, 0.f), fmaxf(z2.y, 0.f))));
 }
 __device__ __forceinline__ float2 clamp2(float2 g2, float lb2) {
   return make_float2(fmaxf(g2.x, lb2), fmaxf(g2.y, lb2));
 }
 
-// 1 - a^2 for a = 2^g2: -expm1(2 g) by its polynomial where a^2 >= e^(-1/2), since the difference
-// loses what slow channels are made of there
+// 1 - a^2 for a = 2^g2, at least the smallest normal number: by the polynomial for exp(2 g) - 1 where
+// a^2 >= e^(-1/2), since the difference loses what slow channels are made of there.  A channel that
+// is wide open (a = 1) so lets in 1e-19 of its input, which is nothing, and needs no case of its own.
 __device__ __forceinline__ float2 one_minus_sq(float2 g2, float2 a) {
-  const float2 y = mul2(g2, both(2.f * kLn2));
-  const float2 near = mul2(mul2(y, both(-1.f)), expm1_ratio(y));
-  const float2 far = fma2(mul2(a, both(-1.f)), a, both(1.f));
-  return make_float2(y.x > -0.5f ? near.x : far.x, y.y > -0.5f ? near.y : far.y);
+  const float2 t = mul2(g2, both(-2.f * kLn2));
+  const float2 near = mul2(t, one_minus_exp_ratio(t));
+  const float2 u = make_float2(t.x < 0.5f ? near.x : fmaf(-a.x, a.x, 1.f), t.y < 0.5f ? near.y : fmaf(-a.y, a.y, 1.f));
+  return make_float2(fmaxf(u.x, kTiny), fmaxf(u.y, kTiny));
 }
-// 1 / sqrt(u), and sqrt(u) = u / sqrt(u); both 0 below the normal range (nothing is let in there,
-// and the gradient's limit is 0).  One Newton step takes the approximate reciprocal root to fp32 accuracy.
-__device__ __forceinline__ void roots(float2 u, float2& r, float2& s) {
-  const float2 r0 = make_float2(u.x > kTiny ? rsq(u.x) : 0.f, u.y > kTiny ? rsq(u.y) : 0.f);
-  const float2 h = mul2(mul2(u, both(-0.5f)), r0);
-  r = mul2(r0, fma2(h, r0, both(1.5f)));
-  s = mul2(u, r);
-}
+__device__ __forceinline__ float2 rsq2(float2 u) { return make_float2(rsq(u.x), rsq(u.y)); }
+
+// sigmoid(x), or x itself where it is a probability already
+__device__ __forceinline__ float beta_fast(float x, bool prob) { return prob ? x : rcp(1.f + ex2(-x * kLog2e)); }
 
 // four consecutive channels of an input row in shared or global memory
 __device__ __forceinline__ void unpack4(const __nv_bfloat16* p, float2& lo, float2& hi) {

@@ -9,6 +9,7 @@ namespace {
 
 constexpr uint32_t kGlrFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_INPUT_NORM;
 constexpr uint32_t kTreeFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_STATE_V_FIRST;
+constexpr int64_t kMaxTokens = INT32_MAX - 1024;  // the recurrence counts in whole tiles past the end
 constexpr int32_t kMaxNodes = 64;
 constexpr int32_t kMaxCopies = 8192;  // pairs of one simultaneous copy: 16 bytes of each fit shared memory
 
@@ -28,7 +29,7 @@ kda_status_t glr_types(kda_dtype_t x, kda_dtype_t gate, kda_dtype_t out) {
 }
 
 size_t glr_partial_bytes(int64_t T, int32_t batch, int32_t H, int32_t d) {
-  if (T < 0 || T > INT32_MAX || batch <= 0 || H <= 0 || d <= 0 || d > 128) return 0;
+  if (T < 0 || T > kMaxTokens || batch <= 0 || H <= 0 || d <= 0 || d > 128) return 0;
   return (size_t)kda::glr_bwd_partials(batch, T, H) * H * (d + 1) * sizeof(float);
 }
 
@@ -45,7 +46,7 @@ extern "C" kda_status_t kda_glr_fwd(const void* x, kda_dtype_t x_dtype, const vo
                                     const int32_t* state_indices, void* out, kda_dtype_t out_dtype,
                                     float* checkpoints, uint32_t flags, float gate_lower_bound,
                                     int32_t* device_status, void* stream) {
-  if (batch < 0 || total_tokens < 0 || total_tokens > INT32_MAX || num_heads <= 0 || d <= 0 || max_slots <= 0)
+  if (batch < 0 || total_tokens < 0 || total_tokens > kMaxTokens || num_heads <= 0 || d <= 0 || max_slots <= 0)
     return KDA_ERR_INVALID_ARG;
   if ((flags & ~kGlrFlags) != 0) return KDA_ERR_INVALID_ARG;
   if (!cu_seqlens || !state_pool || !state_indices || !a_log || !dt_bias) return KDA_ERR_INVALID_ARG;
@@ -128,7 +129,7 @@ extern "C" kda_status_t kda_glr_bwd(const void* dout, kda_dtype_t out_dtype, con
                                     float* dbeta, float* da_log, float* ddt_bias, float* d_initial, uint32_t flags,
                                     float gate_lower_bound, void* workspace, size_t workspace_bytes,
                                     int32_t* device_status, void* stream) {
-  if (batch < 0 || total_tokens < 0 || total_tokens > INT32_MAX || num_heads <= 0 || d <= 0) return KDA_ERR_INVALID_ARG;
+  if (batch < 0 || total_tokens < 0 || total_tokens > kMaxTokens || num_heads <= 0 || d <= 0) return KDA_ERR_INVALID_ARG;
   if ((flags & ~kGlrFlags) != 0) return KDA_ERR_INVALID_ARG;
   if (!cu_seqlens || !a_log || !dt_bias || !da_log || !ddt_bias) return KDA_ERR_INVALID_ARG;
   if (batch > 0 && (!d_initial || !checkpoints)) return KDA_ERR_INVALID_ARG;
