@@ -203,11 +203,49 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _on_device(device):
-    """Makes ``device`` the current one for a launch, at no cost where it already is."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The calls that serve single tokens take a few microseconds on the device, so their wrappers check
+# each tensor in one go and leave it to the functions above to say what is wrong.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _need(t, name, dtype, shape, dev, index):
+    """The address of a contiguous CUDA tensor of this type and shape on device ``index``."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _shape(_dev(t, name, dtype, dev), name, shape)
+    return t.data_ptr()
+
+
+def _where(t, name):
+    """The device of a call's first tensor, and its number."""
+    dev = _dev(t, name).device
+    return dev, dev.index
+
+
+def _on_stream(stream, index):
+    """The address of the stream to launch on, ``stream`` or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _on_device(index):
+    """Makes device ``index`` the current one for a launch, at no cost where it already is."""
+    return _HERE_ALREADY if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _used_on(stream, index, *tensors):
+    """Tells the allocator that tensors made here are in use on ``stream`` (see _Owned)."""
+    if stream is not None and stream != torch.cuda.current_stream(index):
+        for t in tensors:
+            if t is not None and t.numel():
+                t.record_stream(stream)
 
 
 class _Owned:

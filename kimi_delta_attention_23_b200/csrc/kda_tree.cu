@@ -369,8 +369,10 @@ __global__ void __launch_bounds__(kThreads, 2) commit_kernel(const TreeArgs p) {
 
 template <typename Kernel>
 cudaError_t launch(Kernel kernel, const TreeArgs& a, size_t smem, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   kernel<<<(unsigned)((int64_t)a.batch * a.Hv), kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }

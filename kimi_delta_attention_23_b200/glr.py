@@ -19,7 +19,8 @@ import ctypes
 
 import torch
 
-from . import (_DTYPES, KdaError, _dev, _flags, _on_device, _Owned, _ptr, _shape, _stream, load_library)
+from . import (_DTYPES, KdaError, _dev, _flags, _need, _on_device, _on_stream, _used_on, _where,
+               load_library)
 
 __all__ = ["kda_glr_fwd", "kda_glr_bwd", "kda_glr_decode", "kda_glr_checkpoint_shape", "kda_glr_bwd_workspace_size"]
 
@@ -49,50 +50,66 @@ def kda_glr_bwd_workspace_size(total_tokens, batch, num_heads, d) -> int:
     return int(load_library().kda_glr_bwd_workspace_size(total_tokens, batch, num_heads, d))
 
 
+_FLAGS = {}
+
+
 def _glr_flags(gate_mode, beta_mode, input_mode):
-    if input_mode not in ("unit", "norm"):
-        raise ValueError(f"input_mode must be 'unit' or 'norm', got {input_mode!r}")
-    return _flags(gate_mode, beta_mode, "K_FIRST") | (INPUT_NORM if input_mode == "norm" else 0)
+    key = (gate_mode, beta_mode, input_mode)
+    if key not in _FLAGS:
+        if input_mode not in ("unit", "norm"):
+            raise ValueError(f"input_mode must be 'unit' or 'norm', got {input_mode!r}")
+        _FLAGS[key] = _flags(gate_mode, beta_mode, "K_FIRST") | (INPUT_NORM if input_mode == "norm" else 0)
+    return _FLAGS[key]
 
 
 def _inputs(x, raw_gate, beta_logits, a_log, dt_bias):
-    """Checks what all three calls read; returns the device and x's shape."""
-    dev = _dev(x, "x").device
+    """Checks what all three calls read; returns the device, its number, x's shape and the addresses."""
+    dev, index = _where(x, "x")
     if x.dtype not in _DTYPES:
         raise ValueError("x must be float32 or bfloat16")
     if x.dim() != 3:
         raise ValueError(f"x has shape {tuple(x.shape)}, expected [tokens, heads, d]")
     T, H, d = x.shape
-    _shape(_dev(raw_gate, "raw_gate", None, dev), "raw_gate", (T, H, d))
-    if raw_gate.dtype not in _DTYPES or (x.dtype == torch.float32 and raw_gate.dtype != torch.float32):
+    gate_dtype = getattr(raw_gate, "dtype", None)
+    if gate_dtype not in _DTYPES or (x.dtype == torch.float32 and gate_dtype != torch.float32):
+        _dev(raw_gate, "raw_gate", None, dev)
         raise ValueError("raw_gate must be float32, or bfloat16 beside a bfloat16 x")
-    _shape(_dev(beta_logits, "beta_logits", torch.float32, dev), "beta_logits", (T, H))
-    _shape(_dev(a_log, "a_log", torch.float32, dev), "a_log", (H,))
-    _shape(_dev(dt_bias, "dt_bias", torch.float32, dev), "dt_bias", (H, d))
-    return dev, T, H, d
+    return dev, index, T, H, d, (x.data_ptr(), _DTYPES[x.dtype],
+                                 _need(raw_gate, "raw_gate", gate_dtype, (T, H, d), dev, index), _DTYPES[gate_dtype],
+                                 _need(beta_logits, "beta_logits", torch.float32, (T, H), dev, index),
+                                 _need(a_log, "a_log", torch.float32, (H,), dev, index),
+                                 _need(dt_bias, "dt_bias", torch.float32, (H, d), dev, index))
 
 
-def _pool(state_pool, state_indices, dev, B, H, d):
+def _offsets(cu_seqlens, dev, index):
+    _dev(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold B + 1 offsets")
+    return cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+
+
+def _pool(state_pool, state_indices, dev, index, B, H, d):
     _dev(state_pool, "state_pool", torch.float32, dev)
-    if state_pool.dim() != 3 or tuple(state_pool.shape[1:]) != (H, d):
+    if state_pool.dim() != 3 or state_pool.shape[1] != H or state_pool.shape[2] != d:
         raise ValueError(f"state_pool has shape {tuple(state_pool.shape)}, expected [slots, {H}, {d}]")
-    _shape(_dev(state_indices, "state_indices", torch.int32, dev), "state_indices", (B,))
+    return (state_pool.data_ptr(), state_pool.shape[0],
+            _need(state_indices, "state_indices", torch.int32, (B,), dev, index))
 
 
-def _output(out, output_dtype, x, own):
+def _output(out, output_dtype, x, dev, index):
+    """The output (made here if ``out`` is None), its address and type."""
     if output_dtype is None:
         output_dtype = x.dtype if out is None else out.dtype
     if output_dtype not in _DTYPES or (x.dtype == torch.float32 and output_dtype != torch.float32):
         raise ValueError("output_dtype must be float32, or bfloat16 beside a bfloat16 x")
     if out is None:
-        out = own.empty(x.shape, dtype=output_dtype, device=x.device)
-    _shape(_dev(out, "out", output_dtype, x.device), "out", x.shape)
-    return out
+        out = torch.empty_like(x, dtype=output_dtype)
+        return out, out.data_ptr(), _DTYPES[output_dtype]
+    return out, _need(out, "out", output_dtype, x.shape, dev, index), _DTYPES[output_dtype]
 
 
-def _status(device_status, dev):
-    if device_status is not None:
-        _shape(_dev(device_status, "device_status", torch.int32, dev), "device_status", (1,))
+def _status(device_status, dev, index):
+    return None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
 
 
 def kda_glr_fwd(x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices, out=None, *,
@@ -106,26 +123,20 @@ def kda_glr_fwd(x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool
     ``checkpoints`` (f32, kda_glr_checkpoint_shape(T, B, H, d)) keeps what kda_glr_bwd needs.
     """
     lib = load_library()
-    dev, T, H, d = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
-    own = _Owned(stream, dev)
-    _dev(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must hold B + 1 offsets")
-    B = cu_seqlens.numel() - 1
-    _pool(state_pool, state_indices, dev, B, H, d)
-    out = _output(out, output_dtype, x, own)
+    dev, index, T, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    B, cu = _offsets(cu_seqlens, dev, index)
+    pool, slots, indices = _pool(state_pool, state_indices, dev, index, B, H, d)
+    kept = None
     if checkpoints is not None:
-        _shape(_dev(checkpoints, "checkpoints", torch.float32, dev), "checkpoints",
-               (lib.kda_glr_checkpoints(T, B), H, d))
-    _status(device_status, dev)
-    flags = _glr_flags(gate_mode, beta_mode, input_mode)
-    with _on_device(dev):
-        rc = lib.kda_glr_fwd(_ptr(x), _DTYPES[x.dtype], _ptr(raw_gate), _DTYPES[raw_gate.dtype], _ptr(beta_logits),
-                             _ptr(a_log), _ptr(dt_bias), _ptr(cu_seqlens), B, T, H, d, _ptr(state_pool),
-                             state_pool.shape[0], _ptr(state_indices), _ptr(out), _DTYPES[out.dtype],
-                             _ptr(checkpoints), flags, float(gate_lower_bound), _ptr(device_status),
-                             _stream(stream, dev))
-    own.launched()
+        kept = _need(checkpoints, "checkpoints", torch.float32, (lib.kda_glr_checkpoints(T, B), H, d), dev, index)
+    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, dev, index)
+    given = out
+    out, to, out_type = _output(out, output_dtype, x, dev, index)
+    with _on_device(index):
+        rc = lib.kda_glr_fwd(*inputs, cu, B, T, H, d, pool, slots, indices, to, out_type, kept, flags, gate_lower_bound,
+                             status, _on_stream(stream, index))
+    if given is None:
+        _used_on(stream, index, out)
     if rc != 0:
         raise KdaError(rc, "kda_glr_fwd")
     return out
@@ -136,18 +147,16 @@ def kda_glr_decode(x, raw_gate, beta_logits, a_log, dt_bias, state_pool, state_i
                    device_status=None, stream=None):
     """One token of each sequence: x, raw_gate [B,H,d]; beta_logits [B,H]; the rest as kda_glr_fwd."""
     lib = load_library()
-    dev, B, H, d = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
-    own = _Owned(stream, dev)
-    _pool(state_pool, state_indices, dev, B, H, d)
-    out = _output(out, output_dtype, x, own)
-    _status(device_status, dev)
-    flags = _glr_flags(gate_mode, beta_mode, input_mode)
-    with _on_device(dev):
-        rc = lib.kda_glr_decode(_ptr(x), _DTYPES[x.dtype], _ptr(raw_gate), _DTYPES[raw_gate.dtype], _ptr(beta_logits),
-                                _ptr(a_log), _ptr(dt_bias), B, H, d, _ptr(state_pool), state_pool.shape[0],
-                                _ptr(state_indices), _ptr(out), _DTYPES[out.dtype], flags, float(gate_lower_bound),
-                                _ptr(device_status), _stream(stream, dev))
-    own.launched()
+    dev, index, B, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    pool, slots, indices = _pool(state_pool, state_indices, dev, index, B, H, d)
+    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, dev, index)
+    given = out
+    out, to, out_type = _output(out, output_dtype, x, dev, index)
+    with _on_device(index):
+        rc = lib.kda_glr_decode(*inputs, B, H, d, pool, slots, indices, to, out_type, flags, gate_lower_bound, status,
+                                _on_stream(stream, index))
+    if given is None:
+        _used_on(stream, index, out)
     if rc != 0:
         raise KdaError(rc, "kda_glr_decode")
     return out
@@ -168,43 +177,40 @@ def kda_glr_bwd(dout, x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, chec
     allocated when not given.
     """
     lib = load_library()
-    dev, T, H, d = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
-    own = _Owned(stream, dev)
-    _shape(_dev(dout, "dout", None, dev), "dout", (T, H, d))
-    if dout.dtype not in _DTYPES or (x.dtype == torch.float32 and dout.dtype != torch.float32):
+    dev, index, T, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    dtype = getattr(dout, "dtype", None)
+    if dtype not in _DTYPES or (x.dtype == torch.float32 and dtype != torch.float32):
+        _dev(dout, "dout", None, dev)
         raise ValueError("dout must be float32, or bfloat16 beside a bfloat16 x")
-    _dev(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must hold B + 1 offsets")
-    B = cu_seqlens.numel() - 1
-    _shape(_dev(checkpoints, "checkpoints", torch.float32, dev), "checkpoints", (lib.kda_glr_checkpoints(T, B), H, d))
-    if d_final is not None:
-        _shape(_dev(d_final, "d_final", torch.float32, dev), "d_final", (B, H, d))
+    douts = _need(dout, "dout", dtype, (T, H, d), dev, index)
+    B, cu = _offsets(cu_seqlens, dev, index)
+    kept = _need(checkpoints, "checkpoints", torch.float32, (lib.kda_glr_checkpoints(T, B), H, d), dev, index)
+    final = None if d_final is None else _need(d_final, "d_final", torch.float32, (B, H, d), dev, index)
+    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, dev, index)
+    made = []
 
     def grad(t, name, shape, dtype=torch.float32):
         if t is None:
-            return own.empty(shape, dtype=dtype, device=dev)
-        _shape(_dev(t, name, dtype, dev), name, shape)
-        return t
+            t = torch.empty(shape, dtype=dtype, device=dev)
+            made.append(t)
+            return t, t.data_ptr()
+        return t, _need(t, name, dtype, shape, dev, index)
 
-    dx = grad(dx, "dx", (T, H, d), x.dtype)
-    draw_gate = grad(draw_gate, "draw_gate", (T, H, d), raw_gate.dtype)
-    dbeta = grad(dbeta, "dbeta", (T, H))
-    da_log = grad(da_log, "da_log", (H,))
-    ddt_bias = grad(ddt_bias, "ddt_bias", (H, d))
-    d_initial = grad(d_initial, "d_initial", (B, H, d))
-    _status(device_status, dev)
-    flags = _glr_flags(gate_mode, beta_mode, input_mode)
-    with _on_device(dev):
+    dx, dxs = grad(dx, "dx", (T, H, d), x.dtype)
+    draw_gate, draws = grad(draw_gate, "draw_gate", (T, H, d), raw_gate.dtype)
+    dbeta, dbetas = grad(dbeta, "dbeta", (T, H))
+    da_log, das = grad(da_log, "da_log", (H,))
+    ddt_bias, dbs = grad(ddt_bias, "ddt_bias", (H, d))
+    d_initial, dis = grad(d_initial, "d_initial", (B, H, d))
+    with _on_device(index):
         if workspace is None:
-            workspace = own.empty(lib.kda_glr_bwd_workspace_size(T, B, H, d), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(lib.kda_glr_bwd_workspace_size(T, B, H, d), dtype=torch.uint8, device=dev)
+            made.append(workspace)
         _dev(workspace, "workspace", torch.uint8, dev)
-        rc = lib.kda_glr_bwd(_ptr(dout), _DTYPES[dout.dtype], _ptr(x), _DTYPES[x.dtype], _ptr(raw_gate),
-                             _DTYPES[raw_gate.dtype], _ptr(beta_logits), _ptr(a_log), _ptr(dt_bias), _ptr(cu_seqlens),
-                             B, T, H, d, _ptr(checkpoints), _ptr(d_final), _ptr(dx), _ptr(draw_gate), _ptr(dbeta),
-                             _ptr(da_log), _ptr(ddt_bias), _ptr(d_initial), flags, float(gate_lower_bound),
-                             _ptr(workspace), workspace.numel(), _ptr(device_status), _stream(stream, dev))
-    own.launched()
+        rc = lib.kda_glr_bwd(douts, _DTYPES[dtype], *inputs, cu, B, T, H, d, kept, final, dxs, draws, dbetas, das, dbs, dis,
+                             flags, gate_lower_bound, workspace.data_ptr(), workspace.numel(), status,
+                             _on_stream(stream, index))
+    _used_on(stream, index, *made)
     if rc != 0:
         raise KdaError(rc, "kda_glr_bwd")
     return {"dx": dx, "draw_gate": draw_gate, "dbeta": dbeta, "da_log": da_log, "ddt_bias": ddt_bias,

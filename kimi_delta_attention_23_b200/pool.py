@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import KdaError, _dev, _on_device, _Owned, _ptr, _shape, _stream, load_library
+from . import KdaError, _dev, _need, _on_device, _on_stream, _used_on, load_library
 
 __all__ = ["kda_pool_copy", "kda_pool_fork", "kda_pool_free", "kda_pool_compact", "kda_pool_workspace_size",
            "MAX_POOL_COPIES"]
@@ -36,35 +36,37 @@ def kda_pool_workspace_size(n, max_slots) -> int:
 
 def _layout(pool, stacked):
     _dev(pool, "state_pool", torch.float32)
-    lead = 2 if stacked else 1
-    if pool.dim() < lead + 1 or pool.numel() == 0:
-        raise ValueError(f"state_pool has shape {tuple(pool.shape)}, expected "
+    shape, lead = pool.shape, 2 if stacked else 1
+    if len(shape) < lead + 1 or pool.numel() == 0:
+        raise ValueError(f"state_pool has shape {tuple(shape)}, expected "
                          f"{'[layers, slots, ...]' if stacked else '[slots, ...]'} with at least one element")
-    layers, slots = (pool.shape[0], pool.shape[1]) if stacked else (1, pool.shape[0])
+    layers, slots = (shape[0], shape[1]) if stacked else (1, shape[0])
     return pool.device, layers, slots, pool.numel() // (layers * slots)
 
 
 def _list(t, name, dev, n=None):
+    """The length and address of a list of slots."""
+    if n is not None:
+        return n, _need(t, name, torch.int32, (n,), dev, dev.index)
     _dev(t, name, torch.int32, dev)
     if t.dim() != 1:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected one dimension")
-    if n is not None:
-        _shape(t, name, (n,))
-    return t.numel()
+    return t.numel(), t.data_ptr()
 
 
-def _call(what, pool, layers, slots, elems, lists, n, results, workspace, device_status, stream, own, dev):
-    lib = load_library()
-    if device_status is not None:
-        _shape(_dev(device_status, "device_status", torch.int32, dev), "device_status", (1,))
-    with _on_device(dev):
+def _call(what, pool, layout, lists, n, results, workspace, device_status, stream, made=()):
+    dev, layers, slots, elems = layout
+    index, lib = dev.index, load_library()
+    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
+    with _on_device(index):
         if workspace is None:
-            workspace = own.empty(lib.kda_pool_workspace_size(n, slots), dtype=torch.uint8, device=dev)
-        _dev(workspace, "workspace", torch.uint8, dev)
-        rc = getattr(lib, what)(_ptr(pool), layers, slots, elems, *[_ptr(t) for t in lists], n,
-                                *[_ptr(t) for t in results], _ptr(workspace), workspace.numel(), _ptr(device_status),
-                                _stream(stream, dev))
-    own.launched()
+            workspace = torch.empty(lib.kda_pool_workspace_size(n, slots), dtype=torch.uint8, device=dev)
+            made = (*made, workspace)
+        else:
+            _dev(workspace, "workspace", torch.uint8, dev)
+        rc = getattr(lib, what)(pool.data_ptr(), layers, slots, elems, *lists, n, *results, workspace.data_ptr(),
+                                workspace.numel(), status, _on_stream(stream, index))
+    _used_on(stream, index, *made)
     if rc != 0:
         raise KdaError(rc, what)
 
@@ -75,13 +77,12 @@ def kda_pool_copy(state_pool, src, dst, *, stacked=False, workspace=None, device
     ``src``, ``dst`` [n] i32, n <= 8192.  Slots out of range, and a destination that is named again
     (its first pair counts), are reported in ``device_status`` and skipped.
     """
-    dev, layers, slots, elems = _layout(state_pool, stacked)
-    n = _list(src, "src", dev)
-    _list(dst, "dst", dev, n)
+    layout = dev, _, _, _ = _layout(state_pool, stacked)
+    n, srcs = _list(src, "src", dev)
+    _, dsts = _list(dst, "dst", dev, n)
     if n > MAX_POOL_COPIES:
         raise ValueError(f"at most {MAX_POOL_COPIES} pairs per call, got {n}")
-    _call("kda_pool_copy", state_pool, layers, slots, elems, (src, dst), n, (), workspace, device_status, stream,
-          _Owned(stream, dev), dev)
+    _call("kda_pool_copy", state_pool, layout, (srcs, dsts), n, (), workspace, device_status, stream)
 
 
 def kda_pool_fork(state_pool, live, src, dst=None, *, stacked=False, workspace=None, device_status=None, stream=None):
@@ -90,15 +91,15 @@ def kda_pool_fork(state_pool, live, src, dst=None, *, stacked=False, workspace=N
     The lowest free slots are taken in the order of the list.  A source that is not live, or one for
     which no slot is left, is reported in ``device_status`` and gets -1.
     """
-    dev, layers, slots, elems = _layout(state_pool, stacked)
-    own = _Owned(stream, dev)
-    _list(live, "live", dev, slots)
-    n = _list(src, "src", dev)
+    layout = dev, _, slots, _ = _layout(state_pool, stacked)
+    _, lives = _list(live, "live", dev, slots)
+    n, srcs = _list(src, "src", dev)
+    made = ()
     if dst is None:
-        dst = own.empty(n, dtype=torch.int32, device=dev)
-    _list(dst, "dst", dev, n)
-    _call("kda_pool_fork", state_pool, layers, slots, elems, (live, src, dst), n, (), workspace, device_status, stream,
-          own, dev)
+        dst = torch.empty_like(src)
+        made = (dst,)
+    _, dsts = _list(dst, "dst", dev, n)
+    _call("kda_pool_fork", state_pool, layout, (lives, srcs, dsts), n, (), workspace, device_status, stream, made)
     return dst
 
 
@@ -107,11 +108,10 @@ def kda_pool_free(state_pool, live, slots, *, stacked=False, workspace=None, dev
 
     A slot that is not live, or is listed again, is reported in ``device_status`` and left alone.
     """
-    dev, layers, max_slots, elems = _layout(state_pool, stacked)
-    _list(live, "live", dev, max_slots)
-    n = _list(slots, "slots", dev)
-    _call("kda_pool_free", state_pool, layers, max_slots, elems, (live, slots), n, (), workspace, device_status, stream,
-          _Owned(stream, dev), dev)
+    layout = dev, _, max_slots, _ = _layout(state_pool, stacked)
+    _, lives = _list(live, "live", dev, max_slots)
+    n, listed = _list(slots, "slots", dev)
+    _call("kda_pool_free", state_pool, layout, (lives, listed), n, (), workspace, device_status, stream)
 
 
 def kda_pool_compact(state_pool, live, state_indices, num_live=None, *, stacked=False, workspace=None,
@@ -123,13 +123,13 @@ def kda_pool_compact(state_pool, live, state_indices, num_live=None, *, stacked=
     new places; an index that names no live slot is reported in ``device_status`` and kept.  What is
     left in the slots above is unspecified.
     """
-    dev, layers, slots, elems = _layout(state_pool, stacked)
-    own = _Owned(stream, dev)
-    _list(live, "live", dev, slots)
-    n = _list(state_indices, "state_indices", dev)
+    layout = dev, _, slots, _ = _layout(state_pool, stacked)
+    _, lives = _list(live, "live", dev, slots)
+    n, indices = _list(state_indices, "state_indices", dev)
+    made = ()
     if num_live is None:
-        num_live = own.empty(1, dtype=torch.int32, device=dev)
-    _list(num_live, "num_live", dev, 1)
-    _call("kda_pool_compact", state_pool, layers, slots, elems, (live, state_indices), n, (num_live,), workspace,
-          device_status, stream, own, dev)
+        num_live = torch.empty(1, dtype=torch.int32, device=dev)
+        made = (num_live,)
+    _, counts = _list(num_live, "num_live", dev, 1)
+    _call("kda_pool_compact", state_pool, layout, (lives, indices), n, (counts,), workspace, device_status, stream, made)
     return num_live

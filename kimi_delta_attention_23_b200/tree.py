@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from . import (_DTYPES, KdaError, _dev, _flags, _on_device, _Owned, _ptr, _shape, _stream, load_library)
+from . import (_DTYPES, KdaError, _dev, _flags, _need, _on_device, _on_stream, _used_on, _where, load_library)
 
 __all__ = ["kda_tree_decode", "kda_tree_commit", "MAX_TREE_NODES"]
 
@@ -27,24 +27,35 @@ SIGNATURES = {
 }
 
 
-def _tree(cu_nodes, parents, max_nodes, M, dev):
+_FLAGS = {}
+
+
+def _tree_flags(gate_mode, beta_mode, state_layout):
+    key = (gate_mode, beta_mode, state_layout)
+    if key not in _FLAGS:
+        _FLAGS[key] = _flags(*key)
+    return _FLAGS[key]
+
+
+def _tree(cu_nodes, parents, max_nodes, M, dev, index):
     _dev(cu_nodes, "cu_nodes", torch.int32, dev)
     if cu_nodes.dim() != 1 or cu_nodes.numel() < 1:
         raise ValueError("cu_nodes must hold B + 1 offsets")
-    _shape(_dev(parents, "parents", torch.int32, dev), "parents", (M,))
     if max_nodes is None:
         max_nodes = max(1, min(M, MAX_TREE_NODES))
     if not 1 <= max_nodes <= MAX_TREE_NODES:
         raise ValueError(f"max_nodes must be 1 .. {MAX_TREE_NODES}, got {max_nodes}")
-    return cu_nodes.numel() - 1, int(max_nodes)
+    return (cu_nodes.numel() - 1, int(max_nodes), cu_nodes.data_ptr(),
+            _need(parents, "parents", torch.int32, (M,), dev, index))
 
 
-def _pool(state_pool, state_indices, state_layout, dev, B, Hv, dk, dv):
+def _pool(state_pool, state_indices, state_layout, dev, index, B, Hv, dk, dv):
     blk = (Hv, dk, dv) if state_layout == "K_FIRST" else (Hv, dv, dk)
     _dev(state_pool, "state_pool", torch.float32, dev)
-    if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != blk:
+    if state_pool.dim() != 4 or state_pool.shape[1:] != blk:
         raise ValueError(f"state_pool has shape {tuple(state_pool.shape)}, expected [slots, {blk}]")
-    _shape(_dev(state_indices, "state_indices", torch.int32, dev), "state_indices", (B,))
+    return (state_pool.data_ptr(), state_pool.shape[0],
+            _need(state_indices, "state_indices", torch.int32, (B,), dev, index))
 
 
 def kda_tree_decode(q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_nodes, parents, state_pool, state_indices,
@@ -61,44 +72,44 @@ def kda_tree_decode(q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_nodes, pa
     deltas [M,Hv,dv] f32), the second for kda_tree_commit.
     """
     lib = load_library()
-    dev = _dev(q, "q").device
-    own = _Owned(stream, dev)
-    if q.dtype not in _DTYPES:
+    dev, index = _where(q, "q")
+    dtype = q.dtype
+    if dtype not in _DTYPES:
         raise ValueError("q/k/v must be float32 or bfloat16")
     if q.dim() != 3:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected [M, Hk, dk]")
     M, Hk, dk = q.shape
-    _shape(_dev(k, "k", q.dtype, dev), "k", (M, Hk, dk))
-    _dev(v, "v", q.dtype, dev)
+    ks = _need(k, "k", dtype, (M, Hk, dk), dev, index)
+    _dev(v, "v", dtype, dev)
     if v.dim() != 3 or v.shape[0] != M:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected [{M}, Hv, dv]")
-    Hv, dv = v.shape[1], v.shape[2]
-    _shape(_dev(raw_gate, "raw_gate", torch.float32, dev), "raw_gate", (M, Hv, dk))
-    _shape(_dev(beta_logits, "beta_logits", torch.float32, dev), "beta_logits", (M, Hv))
-    _shape(_dev(a_log, "a_log", torch.float32, dev), "a_log", (Hv,))
-    _shape(_dev(dt_bias, "dt_bias", torch.float32, dev), "dt_bias", (Hv, dk))
-    B, max_nodes = _tree(cu_nodes, parents, max_nodes, M, dev)
-    flags = _flags(gate_mode, beta_mode, state_layout)
-    _pool(state_pool, state_indices, state_layout, dev, B, Hv, dk, dv)
+    _, Hv, dv = v.shape
+    raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), dev, index)
+    betas = _need(beta_logits, "beta_logits", torch.float32, (M, Hv), dev, index)
+    alogs = _need(a_log, "a_log", torch.float32, (Hv,), dev, index)
+    biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), dev, index)
+    B, max_nodes, cu, pars = _tree(cu_nodes, parents, max_nodes, M, dev, index)
+    flags = _tree_flags(gate_mode, beta_mode, state_layout)
+    pool, slots, indices = _pool(state_pool, state_indices, state_layout, dev, index, B, Hv, dk, dv)
     if output_dtype is None:
         output_dtype = v.dtype if out is None else out.dtype
     if output_dtype not in _DTYPES:
         raise ValueError("output_dtype must be float32 or bfloat16")
+    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
+    made = []
     if out is None:
-        out = own.empty((M, Hv, dv), dtype=output_dtype, device=dev)
-    _shape(_dev(out, "out", output_dtype, dev), "out", (M, Hv, dv))
+        out = torch.empty_like(v, dtype=output_dtype)
+        made.append(out)
     if deltas is None:
-        deltas = own.empty((M, Hv, dv), dtype=torch.float32, device=dev)
-    _shape(_dev(deltas, "deltas", torch.float32, dev), "deltas", (M, Hv, dv))
-    if device_status is not None:
-        _shape(_dev(device_status, "device_status", torch.int32, dev), "device_status", (1,))
-    with _on_device(dev):
-        rc = lib.kda_tree_decode(_ptr(q), _ptr(k), _ptr(v), _DTYPES[q.dtype], _ptr(raw_gate), _ptr(beta_logits),
-                                 _ptr(a_log), _ptr(dt_bias), _ptr(cu_nodes), _ptr(parents), B, M, max_nodes, Hk, Hv,
-                                 dk, dv, _ptr(state_pool), state_pool.shape[0], _ptr(state_indices), _ptr(out),
-                                 _DTYPES[output_dtype], _ptr(deltas), flags, float(gate_lower_bound),
-                                 _ptr(device_status), _stream(stream, dev))
-    own.launched()
+        deltas = torch.empty_like(v, dtype=torch.float32)
+        made.append(deltas)
+    with _on_device(index):
+        rc = lib.kda_tree_decode(q.data_ptr(), ks, v.data_ptr(), _DTYPES[dtype], raws, betas, alogs, biases, cu, pars, B, M,
+                                 max_nodes, Hk, Hv, dk, dv, pool, slots, indices,
+                                 _need(out, "out", output_dtype, (M, Hv, dv), dev, index), _DTYPES[output_dtype],
+                                 _need(deltas, "deltas", torch.float32, (M, Hv, dv), dev, index), flags,
+                                 gate_lower_bound, status, _on_stream(stream, index))
+    _used_on(stream, index, *made)
     if rc != 0:
         raise KdaError(rc, "kda_tree_decode")
     return out, deltas
@@ -113,7 +124,7 @@ def kda_tree_commit(k, raw_gate, a_log, dt_bias, deltas, cu_nodes, parents, acce
     state stays).  The other tensors as in the kda_tree_decode call that returned ``deltas``.
     """
     lib = load_library()
-    dev = _dev(k, "k").device
+    dev, index = _where(k, "k")
     if k.dtype not in _DTYPES:
         raise ValueError("k must be float32 or bfloat16")
     if k.dim() != 3:
@@ -122,20 +133,18 @@ def kda_tree_commit(k, raw_gate, a_log, dt_bias, deltas, cu_nodes, parents, acce
     _dev(deltas, "deltas", torch.float32, dev)
     if deltas.dim() != 3 or deltas.shape[0] != M:
         raise ValueError(f"deltas has shape {tuple(deltas.shape)}, expected [{M}, Hv, dv]")
-    Hv, dv = deltas.shape[1], deltas.shape[2]
-    _shape(_dev(raw_gate, "raw_gate", torch.float32, dev), "raw_gate", (M, Hv, dk))
-    _shape(_dev(a_log, "a_log", torch.float32, dev), "a_log", (Hv,))
-    _shape(_dev(dt_bias, "dt_bias", torch.float32, dev), "dt_bias", (Hv, dk))
-    B, max_nodes = _tree(cu_nodes, parents, max_nodes, M, dev)
-    _shape(_dev(accepted, "accepted", torch.int32, dev), "accepted", (B,))
-    flags = _flags(gate_mode, "logits", state_layout)
-    _pool(state_pool, state_indices, state_layout, dev, B, Hv, dk, dv)
-    if device_status is not None:
-        _shape(_dev(device_status, "device_status", torch.int32, dev), "device_status", (1,))
-    with _on_device(dev):
-        rc = lib.kda_tree_commit(_ptr(k), _DTYPES[k.dtype], _ptr(raw_gate), _ptr(a_log), _ptr(dt_bias), _ptr(deltas),
-                                 _ptr(cu_nodes), _ptr(parents), _ptr(accepted), B, M, max_nodes, Hk, Hv, dk, dv,
-                                 _ptr(state_pool), state_pool.shape[0], _ptr(state_indices), flags,
-                                 float(gate_lower_bound), _ptr(device_status), _stream(stream, dev))
+    _, Hv, dv = deltas.shape
+    raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), dev, index)
+    alogs = _need(a_log, "a_log", torch.float32, (Hv,), dev, index)
+    biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), dev, index)
+    B, max_nodes, cu, pars = _tree(cu_nodes, parents, max_nodes, M, dev, index)
+    took = _need(accepted, "accepted", torch.int32, (B,), dev, index)
+    flags = _tree_flags(gate_mode, "logits", state_layout)
+    pool, slots, indices = _pool(state_pool, state_indices, state_layout, dev, index, B, Hv, dk, dv)
+    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
+    with _on_device(index):
+        rc = lib.kda_tree_commit(k.data_ptr(), _DTYPES[k.dtype], raws, alogs, biases, deltas.data_ptr(), cu, pars, took, B, M,
+                                 max_nodes, Hk, Hv, dk, dv, pool, slots, indices, flags, gate_lower_bound, status,
+                                 _on_stream(stream, index))
     if rc != 0:
         raise KdaError(rc, "kda_tree_commit")
