@@ -24,14 +24,18 @@
 //
 // The commit is S' = e^{G_a} o S + sum over the path (k_j o e^{G_a - G_j}) u_j^T, one pass over the
 // state, bound by its 8 dk dv bytes.
-#include "kda_common.cuh"
+#include <type_traits>
+
+#include "kda_glr_math.cuh"
 #include "kda_ops_internal.h"
+#include "kda_sm100.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPitch = 132;    // floats of a node's row in shared memory
+constexpr uint64_t kWaitNs = 1000000000ull;  // limit of the wait for a copy
 constexpr int kPitchH = 144;   // bf16 of a row of the split factors (32 bytes past 256: no conflicts)
 
 // Offsets, slot and parents of a sequence; false where one is out of range.  All threads call it.
@@ -66,24 +70,72 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 
 template <int kNodes>
 struct TreeSmem {
+  // 64 KB: the state (1), then (K o e^G) S and (Q o e^G) S (2), the former becoming the deltas (3)
   union {
-    float k[kNodes][kPitch];   // keys (1)
-    float u[kNodes][kPitch];   // (K o e^G) S (2), then the deltas (3)
+    alignas(128) float state[128 * 128];
+    struct {
+      float u[kNodes][128], qs[kNodes][128];
+    };
   };
+  // keys and decays (1), then the factors of the product with the state (2).  Factor rows 16 t + r:
+  // key row 8 t + r for r < 8, query row 8 t + r - 8 for the others
   union {
-    float al[kNodes][kPitch];  // decays (1)
-    float qs[kNodes][kPitch];  // (Q o e^G) S (2)
+    struct {
+      float k[kNodes][kPitch], al[kNodes][kPitch];
+    };
+    struct {
+      __nv_bfloat16 hi[2 * kNodes][kPitchH], lo[2 * kNodes][kPitchH];
+    };
   };
-  // rows 16 t + r: key row 8 t + r for r < 8, query row 8 t + r - 8 for the others
-  __nv_bfloat16 hi[2 * kNodes][kPitchH], lo[2 * kNodes][kPitchH];
-  float a[kNodes][kNodes + 1], b[kNodes][kNodes + 1];
+  float a[kNodes][kNodes + 4], b[kNodes][kNodes + 4];  // zero where j is no ancestor of i
   float beta[kNodes];
   int32_t par[kNodes];
+  uint64_t full;
 };
 
-template <int kNodes, bool kVFirst, bool kFull>
-__global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs p) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+// four channels of an input row of d, zero past its end.  No branches: a load whose value is converted
+// inside one is waited for there, and the loads of a thread then come one after the other.
+template <bool kWide, typename T>
+__device__ __forceinline__ float4 load_quad(const T* row, int c, int d) {
+  if constexpr (kWide) {
+    float2 lo, hi;
+    glr::unpack4(row + c, lo, hi);
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+  } else {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = glr::to_f32(row[min(c + e, d - 1)]);
+    return make_float4(c < d ? v[0] : 0.f, c + 1 < d ? v[1] : 0.f, c + 2 < d ? v[2] : 0.f, c + 3 < d ? v[3] : 0.f);
+  }
+}
+
+// the sum over j < kCount of row[j] u[j], in four chains
+template <int kCount>
+__device__ __forceinline__ float dot(const float* row, const float* u) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < kCount; j += 4) {
+    const float4 w = *reinterpret_cast<const float4*>(row + j);
+    s[0] = fmaf(w.x, u[j], s[0]);
+    s[1] = fmaf(w.y, u[j + 1], s[1]);
+    s[2] = fmaf(w.z, u[j + 2], s[2]);
+    s[3] = fmaf(w.w, u[j + 3], s[3]);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Blocks of kBlk nodes, one after the other (a loop that the compiler unrolls, since u sits in registers).
+template <int kNodes, int kBlk, int kFirst, typename F>
+__device__ __forceinline__ void each_block(F&& f) {
+  if constexpr (kFirst < kNodes) {
+    f(std::integral_constant<int, kFirst>{});
+    each_block<kNodes, kBlk, kFirst + kBlk>(f);
+  }
+}
+
+template <int kNodes, bool kVFirst, bool kFull, typename T>
+__global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(const TreeArgs p) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   TreeSmem<kNodes>& sm = *reinterpret_cast<TreeSmem<kNodes>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv, kh = h / (p.Hv / p.Hk);
@@ -92,50 +144,79 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs p) {
   if (!tree_of(p, b, m0, n, slot, sm.par)) return;
   if (n == 0) return;
   const float* state = p.pool + ((size_t)slot * p.Hv + h) * (size_t)dk * dv;
-  if constexpr (kFull) {  // the state is wanted after the scores: bring it to L2 meanwhile
-    if (tid == 0)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(state), "r"(128 * 128 * 4) : "memory");
+  if constexpr (kFull) {  // the state comes while the scores are worked out
+    if (tid == 0) {
+      const uint32_t bar = sm100::smem_addr(&sm.full);
+      sm100::mbar_init(bar, 1);
+      sm100::fence_mbar_init();
+      sm100::mbar_arrive_expect_tx(bar, sizeof(sm.state));
+      sm100::bulk_g2s(sm100::smem_addr(sm.state), state, sizeof(sm.state), bar);
+    }
   }
 
-  // ---- keys, decays and beta of all nodes; zero keys past dk
-  const bool safe = p.flags & KDA_GATE_SAFE, prob = p.flags & KDA_BETA_PROB;
+  // ---- keys, decays and beta of all nodes (zero keys past dk); no scores yet
+  const T* qs = reinterpret_cast<const T*>(p.q) + ((size_t)m0 * p.Hk + kh) * dk;
+  const T* ks = reinterpret_cast<const T*>(p.k) + ((size_t)m0 * p.Hk + kh) * dk;
+  const float* raws = p.raw_gate + ((size_t)m0 * p.Hv + h) * dk;
+  const size_t k_row = (size_t)p.Hk * dk, raw_row = (size_t)p.Hv * dk;
   {
-    const float a_log = p.a_log[h];
-    for (int i = tid; i < n * 128; i += kThreads) {
-      const int m = i >> 7, c = i & 127;
-      float kv = 0.f, al = 1.f;
-      if (c < dk) {
-        kv = load_in(p.k, ((size_t)(m0 + m) * p.Hk + kh) * dk + c, p.in_bf16);
-        al = expf(gate_f32(p.raw_gate[((size_t)(m0 + m) * p.Hv + h) * dk + c], a_log, p.dt_bias[(size_t)h * dk + c], safe, p.lb));
+    const glr::HeadGate gate = glr::head_gate(p.a_log[h], p.flags & KDA_GATE_SAFE, p.lb);
+    const int c = 4 * (tid & 31);
+    const float4 bias = load_quad<kFull>(p.dt_bias + (size_t)h * dk, c, dk);
+    const float2 bias0 = glr::mul2(make_float2(bias.x, bias.y), glr::both(glr::kLog2e));
+    const float2 bias1 = glr::mul2(make_float2(bias.z, bias.w), glr::both(glr::kLog2e));
+    constexpr int kAtOnce = kNodes >= 32 ? 4 : kNodes / 8;  // rows of a warp with their loads in flight together
+#pragma unroll 1
+    for (int m1 = warp; m1 < n; m1 += 8 * kAtOnce) {
+      float4 kv[kAtOnce], raw[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int m = min(m1 + 8 * j, n - 1);
+        kv[j] = load_quad<kFull>(ks + m * k_row, c, dk);
+        raw[j] = load_quad<kFull>(raws + m * raw_row, c, dk);
       }
-      sm.k[m][c] = kv;
-      sm.al[m][c] = al;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int m = m1 + 8 * j;
+        if (m < n) {
+          const float2 z0 = glr::pre_log2(make_float2(raw[j].x, raw[j].y), bias0);
+          const float2 z1 = glr::pre_log2(make_float2(raw[j].z, raw[j].w), bias1);
+          const float2 g0 = glr::clamp2(glr::gate_log2(z0, glr::exp_neg_abs(z0), gate.c), gate.lb2);
+          const float2 g1 = glr::clamp2(glr::gate_log2(z1, glr::exp_neg_abs(z1), gate.c), gate.lb2);
+          *reinterpret_cast<float4*>(&sm.k[m][c]) = kv[j];
+          *reinterpret_cast<float4*>(&sm.al[m][c]) = make_float4(glr::ex2(g0.x), glr::ex2(g0.y), glr::ex2(g1.x), glr::ex2(g1.y));
+        }
+      }
     }
-    for (int m = tid; m < n; m += kThreads) sm.beta[m] = beta_f32(p.beta[(size_t)(m0 + m) * p.Hv + h], prob);
+    for (int i = tid; i < kNodes * (kNodes + 4) / 4; i += kThreads) {
+      reinterpret_cast<float4*>(sm.a)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      reinterpret_cast<float4*>(sm.b)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int m = tid; m < n; m += kThreads)
+      sm.beta[m] = beta_f32(p.beta[(size_t)(m0 + m) * p.Hv + h], p.flags & KDA_BETA_PROB);
+  }
+  constexpr int kGroup = kThreads / kNodes;  // lanes per node
+  constexpr int kQuads = 32 / kGroup;        // float4's of channels per lane
+  static_assert(kGroup <= 32 && kQuads >= 1, "");
+  const int node = tid / kGroup, g = tid % kGroup;
+  float4 qq[kQuads];
+#pragma unroll
+  for (int j = 0; j < kQuads; ++j) {
+    qq[j] = load_quad<kFull>(qs + min(node, n - 1) * k_row, 4 * (g + kGroup * j), dk);
+    if (node >= n) qq[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
 
   // ---- 1. scores, and the factors of the product with the state
   {
-    constexpr int kGroup = kThreads / kNodes;  // lanes per node
-    constexpr int kQuads = 32 / kGroup;        // float4's of channels per lane
-    static_assert(kGroup <= 32 && kQuads >= 1, "");
-    const int i = tid / kGroup, g = tid % kGroup;
-    const bool mine = i < n;
-    float4 kq[kQuads], qq[kQuads], w[kQuads];
+    float4 kq[kQuads], w[kQuads];
 #pragma unroll
     for (int j = 0; j < kQuads; ++j) {
-      const int c = 4 * (g + kGroup * j);
       w[j] = make_float4(1.f, 1.f, 1.f, 1.f);
-      kq[j] = qq[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (mine) {
-        kq[j] = *reinterpret_cast<const float4*>(&sm.k[i][c]);
-        const size_t at = ((size_t)(m0 + i) * p.Hk + kh) * dk + c;
-        qq[j] = make_float4(c < dk ? load_in(p.q, at, p.in_bf16) : 0.f, c + 1 < dk ? load_in(p.q, at + 1, p.in_bf16) : 0.f,
-                            c + 2 < dk ? load_in(p.q, at + 2, p.in_bf16) : 0.f, c + 3 < dk ? load_in(p.q, at + 3, p.in_bf16) : 0.f);
-      }
+      kq[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (node < n) kq[j] = *reinterpret_cast<const float4*>(&sm.k[node][4 * (g + kGroup * j)]);
     }
-    int anc = mine ? i : -1;
+    int anc = node < n ? node : -1;
     while (__any_sync(0xffffffffu, anc >= 0)) {
       float sa = 0.f, sb = 0.f;
       if (anc >= 0) {
@@ -157,14 +238,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs p) {
       }
       if (anc >= 0) {
         if (g == 0) {
-          sm.a[i][anc] = sa;  // for anc == i: not used
-          sm.b[i][anc] = sb;
+          if (anc != node) sm.a[node][anc] = sa;
+          sm.b[node][anc] = sb;
         }
         anc = sm.par[anc];
       }
     }
+    __syncthreads();  // keys and decays have been read: the factors take their place
     // rows past the last node are zero: they share 16-row tiles with others
-    const int rk = 16 * (i >> 3) + (i & 7);
+    const int rk = 16 * (node >> 3) + (node & 7);
 #pragma unroll
     for (int j = 0; j < kQuads; ++j) {
       const int c = 4 * (g + kGroup * j);
@@ -179,14 +261,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs p) {
       *reinterpret_cast<uint2*>(&sm.lo[rk + 8][c]) = lo;
     }
   }
-  __syncthreads();
 
   // ---- 2. the product with the state.  A warp owns 16 value columns (two n-tiles: columns
   // 16 warp + 2 (lane / 4) + {0, 1}) over all key channels.  Within each 16 channels a lane's four
   // are 4 (lane % 4) .. + 3 in both operands (the order of the summed index is free), so that its
   // share of V_FIRST states and of the factors is one wide access.
+  if constexpr (kFull) {
+    if (!sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+  }
   {
-    const int q = lane & 3, g = lane >> 2, col = 16 * warp + 2 * g;
+    const int q = lane & 3, gr = lane >> 2, col = 16 * warp + 2 * gr;
     uint32_t bh[8][2][2], bl[8][2][2];  // [k-step][n-tile][register]
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
@@ -195,13 +279,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs p) {
       if constexpr (kFull && kVFirst) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(state + (size_t)(col + t) * 128 + c));
+          const float4 v = *reinterpret_cast<const float4*>(sm.state + (col + t) * 128 + c);
           s[t][0] = v.x, s[t][1] = v.y, s[t][2] = v.z, s[t][3] = v.w;
         }
       } else if constexpr (kFull) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 v = __ldg(reinterpret_cast<const float2*>(state + (size_t)(c + e) * 128 + col));
+          const float2 v = *reinterpret_cast<const float2*>(sm.state + (c + e) * 128 + col);
           s[0][e] = v.x, s[1][e] = v.y;
         }
       } else {
@@ -217,52 +301,109 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeArgs p) {
         split2(s[t][2], s[t][3], bh[ks][t][1], bl[ks][t][1]);
       }
     }
+    __syncthreads();  // the factors are there, and the state has been read: u and qs take its place
     const int tiles = (n + 7) >> 3;
     for (int t = 0; t < tiles; ++t) {
-      float acc[2][4] = {};
+      float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         const int c = 16 * ks + 4 * q;
-        const uint2 h0 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + g][c]);
-        const uint2 h1 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + g + 8][c]);
-        const uint2 l0 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + g][c]);
-        const uint2 l1 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + g + 8][c]);
+        const uint2 h0 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + gr][c]);
+        const uint2 h1 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + gr + 8][c]);
+        const uint2 l0 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + gr][c]);
+        const uint2 l1 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + gr + 8][c]);
         const uint32_t ah[4] = {h0.x, h1.x, h0.y, h1.y}, al[4] = {l0.x, l1.x, l0.y, l1.y};
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-          mma_bf16(acc[nt], al, bh[ks][nt][0], bh[ks][nt][1]);
-          mma_bf16(acc[nt], ah, bl[ks][nt][0], bl[ks][nt][1]);
-          mma_bf16(acc[nt], ah, bh[ks][nt][0], bh[ks][nt][1]);
+          mma_bf16(big[nt], ah, bh[ks][nt][0], bh[ks][nt][1]);
+          mma_bf16(small[nt], al, bh[ks][nt][0], bh[ks][nt][1]);
+          mma_bf16(small[nt], ah, bl[ks][nt][0], bl[ks][nt][1]);
         }
       }
       // accumulator n = 2 (lane % 4) + {0, 1} of tile nt is column 16 warp + 2 n + nt
-      const int c0 = 16 * warp + 4 * q, i = 8 * t + g;
-      *reinterpret_cast<float4*>(&sm.u[i][c0]) = make_float4(acc[0][0], acc[1][0], acc[0][1], acc[1][1]);
-      *reinterpret_cast<float4*>(&sm.qs[i][c0]) = make_float4(acc[0][2], acc[1][2], acc[0][3], acc[1][3]);
+      const int c0 = 16 * warp + 4 * q, i = 8 * t + gr;
+      *reinterpret_cast<float4*>(&sm.u[i][c0]) =
+          make_float4(big[0][0] + small[0][0], big[1][0] + small[1][0], big[0][1] + small[0][1], big[1][1] + small[1][1]);
+      *reinterpret_cast<float4*>(&sm.qs[i][c0]) =
+          make_float4(big[0][2] + small[0][2], big[1][2] + small[1][2], big[0][3] + small[0][3], big[1][3] + small[1][3]);
     }
   }
   __syncthreads();
 
-  // ---- 3. down the tree, a thread per value column; its own column is all it reads
-  if (tid < dv) {
-    for (int i = 0; i < n; ++i) {
-      const size_t at = ((size_t)(m0 + i) * p.Hv + h) * dv + tid;
-      float r = load_in(p.v, at, p.in_bf16) - sm.u[i][tid];
-      for (int j = sm.par[i]; j >= 0; j = sm.par[j]) r = fmaf(-sm.a[i][j], sm.u[j][tid], r);
-      r *= sm.beta[i];
-      sm.u[i][tid] = r;
-      p.deltas[at] = r;
-    }
-  }
-  __syncthreads();
+  // ---- 3. down the tree, a thread per value column and block by block: one half of the CTA solves a
+  // block of nodes while the other half works out the outputs of the block before it.  The sums run
+  // over all earlier nodes, weights being zero where one is no ancestor; a delta that is not finite
+  // must not reach other branches through such a zero, so from the first one on, ancestors are walked.
+  constexpr int kBlk = kNodes < 16 ? kNodes : 16;
   const int col = tid & 127;
-  if (col < dv) {
-    for (int i = tid >> 7; i < n; i += kThreads / 128) {
-      float r = sm.qs[i][col];
-      for (int j = i; j >= 0; j = sm.par[j]) r = fmaf(sm.b[i][j], sm.u[j][col], r);
-      store_out(p.out, ((size_t)(m0 + i) * p.Hv + h) * dv + col, r, p.out_bf16);
+  const bool solving = tid < 128, mine = col < dv;
+  bool walk = false;
+  float u[kNodes];
+  const size_t row = (size_t)p.Hv * dv;
+  const T* vs = reinterpret_cast<const T*>(p.v) + ((size_t)m0 * p.Hv + h) * dv + (mine ? col : 0);
+  each_block<kNodes, kBlk, 0>([&](auto first) {
+    constexpr int i0 = decltype(first)::value;
+    if (i0 >= n) return;
+    const int end = min(n, i0 + kBlk);
+    const size_t at = ((size_t)(m0 + i0) * p.Hv + h) * dv + col;
+    bool odd = false;
+    if (solving) {
+      float v[kBlk];
+#pragma unroll
+      for (int i = 0; i < kBlk; ++i) v[i] = glr::to_f32(vs[min(i0 + i, n - 1) * row]);
+#pragma unroll
+      for (int i = 0; i < kBlk; ++i) v[i] = i0 + i < n && mine ? v[i] - sm.u[i0 + i][col] : 0.f;
+#pragma unroll
+      for (int i = 0; i < kBlk; ++i) {
+        float r = v[i];
+        if (i0 > 0) r -= dot<i0>(sm.a[i0 + i], u);
+#pragma unroll
+        for (int j = 0; j < i; ++j) r = fmaf(-sm.a[i0 + i][i0 + j], u[i0 + j], r);
+        u[i0 + i] = i0 + i < n ? r * sm.beta[i0 + i] : 0.f;
+        odd |= !isfinite(u[i0 + i]);
+      }
     }
-  }
+    walk |= __syncthreads_or(odd) != 0;
+    if (solving && mine) {
+      if (!walk) {
+#pragma unroll
+        for (int i = 0; i < kBlk; ++i) {
+          if (i0 + i < n) {
+            sm.u[i0 + i][col] = u[i0 + i];
+            p.deltas[at + i * row] = u[i0 + i];
+          }
+        }
+      } else {
+        for (int i = i0; i < end; ++i) {
+          float r = glr::to_f32(vs[i * row]) - sm.u[i][col];
+          for (int j = sm.par[i]; j >= 0; j = sm.par[j]) r = fmaf(-sm.a[i][j], sm.u[j][col], r);
+          r *= sm.beta[i];
+          sm.u[i][col] = r;
+          p.deltas[at + (i - i0) * row] = r;
+        }
+      }
+    }
+    __syncthreads();
+    if (!solving && mine) {
+      if (!walk) {
+#pragma unroll
+        for (int i = 0; i < kBlk; ++i) u[i0 + i] = i0 + i < n ? sm.u[i0 + i][col] : 0.f;
+#pragma unroll 4
+        for (int i = 0; i < kBlk; ++i) {
+          if (i0 + i < n) {
+            const float r = sm.qs[i0 + i][col] + dot<i0 + kBlk>(sm.b[i0 + i], u);
+            store_out(p.out, at + i * row, r, p.out_bf16);
+          }
+        }
+      } else {
+        for (int i = i0; i < end; ++i) {
+          float r = sm.qs[i][col];
+          for (int j = i; j >= 0; j = sm.par[j]) r = fmaf(sm.b[i][j], sm.u[j][col], r);
+          store_out(p.out, at + (i - i0) * row, r, p.out_bf16);
+        }
+      }
+    }
+  });
 }
 
 // ------------------------------------------------------------------------------------ commit
@@ -279,7 +420,7 @@ struct CommitSmem {
 // Thread mapping as the single-token step's: warp w takes the stored rows w + 8 m, a lane four columns.
 template <int kNodes, bool kVFirst, bool kFull>
 __global__ void __launch_bounds__(kThreads, 2) commit_kernel(const TreeArgs p) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   CommitSmem<kNodes>& sm = *reinterpret_cast<CommitSmem<kNodes>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv, kh = h / (p.Hv / p.Hk);
@@ -379,15 +520,25 @@ cudaError_t launch(Kernel kernel, const TreeArgs& a, size_t smem, cudaStream_t s
 
 template <int kNodes, bool kCommit>
 cudaError_t pick(const TreeArgs& a, cudaStream_t stream) {
-  const bool full = a.dk == 128 && a.dv == 128 && (reinterpret_cast<uintptr_t>(a.pool) & 15u) == 0;
+  auto on = [](const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+  const bool full = a.dk == 128 && a.dv == 128 && on(a.pool, 16);
   const size_t smem = kCommit ? sizeof(CommitSmem<kNodes>) : sizeof(TreeSmem<kNodes>);
-  auto go = [&](auto kernel) { return launch(kernel, a, smem, stream); };
   if constexpr (kCommit) {
+    auto go = [&](auto kernel) { return launch(kernel, a, smem, stream); };
     if (a.v_first) return full ? go(commit_kernel<kNodes, true, true>) : go(commit_kernel<kNodes, true, false>);
     return full ? go(commit_kernel<kNodes, false, true>) : go(commit_kernel<kNodes, false, false>);
   } else {
-    if (a.v_first) return full ? go(tree_kernel<kNodes, true, true>) : go(tree_kernel<kNodes, true, false>);
-    return full ? go(tree_kernel<kNodes, false, true>) : go(tree_kernel<kNodes, false, false>);
+    auto go = [&](auto kernel) { return launch(kernel, a, smem, stream); };
+    using bf16 = __nv_bfloat16;
+    // the form for 128 x 128 states reads rows in wide accesses: all of them start on 16 bytes (bf16: 8)
+    const size_t in = a.in_bf16 ? 8 : 16;
+    const bool wide = full && on(a.q, in) && on(a.k, in) && on(a.raw_gate, 16) && on(a.dt_bias, 16);
+    if (a.in_bf16) {
+      if (a.v_first) return wide ? go(tree_kernel<kNodes, true, true, bf16>) : go(tree_kernel<kNodes, true, false, bf16>);
+      return wide ? go(tree_kernel<kNodes, false, true, bf16>) : go(tree_kernel<kNodes, false, false, bf16>);
+    }
+    if (a.v_first) return wide ? go(tree_kernel<kNodes, true, true, float>) : go(tree_kernel<kNodes, true, false, float>);
+    return wide ? go(tree_kernel<kNodes, false, true, float>) : go(tree_kernel<kNodes, false, false, float>);
   }
 }
 

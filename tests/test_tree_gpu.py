@@ -163,6 +163,28 @@ def test_siblings_do_not_see_each_other():
         assert R.rel(out[i:i + 1], alone) < TOL
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("node", [0, 3, 20])
+def test_what_is_not_finite_stays_on_its_branch(bad, node):
+    n = 40
+    c = make([n], 1, 1, 128, 128, dtype=BF16, seed=10)
+    ref, ref_deltas, _ = reference(c)
+    par = c["parents"].tolist()
+    hit = {node}
+    for i in range(node + 1, n):
+        if par[i] in hit:
+            hit.add(i)
+    clean = [i for i in range(n) if i not in hit]
+    assert clean or node == 0
+    c["v"][node, 0, 5] = bad
+    out, deltas = decode(c, F32)
+    # column 5 of the node and of what follows it; every other branch and every other column as before
+    assert not bool(torch.isfinite(out[node, 0, 5])) and not bool(torch.isfinite(deltas[node, 0, 5]))
+    assert R.rel(out[clean], ref[clean]) < TOL and R.rel(deltas[clean], ref_deltas[clean]) < TOL
+    others = [j for j in range(128) if j != 5]
+    assert R.rel(out[:, :, others], ref[:, :, others]) < TOL
+
+
 @pytest.mark.parametrize("what", ["slot", "parent of its own", "parent ahead", "parent below -1", "too many", "decreasing",
                                   "past the end"])
 def test_bad_trees_are_reported_and_skipped(what):
