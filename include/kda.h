@@ -566,7 +566,7 @@ KDA_API kda_status_t kda_tree_commit(const void *k, kda_dtype_t k_dtype, const f
  * several layers that share their indices).  Everything is decided on the device, so the calls can
  * be captured.  live [max_slots] int32: nonzero where a slot is in use.  workspace: at least
  * kda_pool_workspace_size(n, max_slots) bytes, 256-byte aligned; calls that may run at once need one
- * each.  Entries of -1 in the lists (both, for a copy) are padding.
+ * each; a copy of up to 256 pairs needs none.  Entries of -1 in the lists (both, for a copy) are padding.
  *
  * kda_pool_copy     slot dst[i] = slot src[i] for all i at once: sources are read as they were before
  *                   the call, whatever the order.  A destination named again is reported and only its

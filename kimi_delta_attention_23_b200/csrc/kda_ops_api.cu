@@ -291,7 +291,9 @@ kda_status_t pool_call(kda::PoolArgs& a, kda::PoolOp op, void* workspace, size_t
   if (!a.pool || a.layers <= 0 || a.max_slots <= 0 || a.slot_elems <= 0 || a.n < 0) return KDA_ERR_INVALID_ARG;
   // element offsets within the stack are 64-bit; their product must be one too
   if (a.slot_elems > INT64_MAX / 4 / a.layers / a.max_slots) return KDA_ERR_INVALID_ARG;
-  if (!work_ok(workspace, workspace_bytes, kda_pool_workspace_size(a.n, a.max_slots))) return KDA_ERR_WORKSPACE;
+  if (kda::pool_needs_work(op, a.n) &&
+      !work_ok(workspace, workspace_bytes, kda_pool_workspace_size(a.n, a.max_slots)))
+    return KDA_ERR_WORKSPACE;
   a.work = reinterpret_cast<int32_t*>(workspace);
   return done(kda::launch_pool(a, op, as_stream(stream)));
 }

@@ -111,6 +111,7 @@ cudaError_t launch_glr_decode(const GlrArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_decode(const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_commit(const TreeArgs& a, cudaStream_t stream);
 size_t pool_work_ints(int32_t n, int32_t max_slots);
+bool pool_needs_work(PoolOp op, int32_t n);
 cudaError_t launch_pool(const PoolArgs& a, PoolOp op, cudaStream_t stream);
 
 }  // namespace kda

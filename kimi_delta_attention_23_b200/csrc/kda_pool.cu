@@ -1,6 +1,6 @@
 // kda_pool.cu -- slots of a state pool copied, forked, freed and packed.
 //
-// Every call is a plan and a move.  The plan (one CTA) checks the request against the pool and
+// Every call is a plan and a move.  The plan (one CTA, or every CTA for itself in a copy of few pairs) checks the request against the pool and
 // writes the list of (source, destination) slots that the move carries out, so nothing about it is
 // known on the host and the calls can be captured.  The move is bound by HBM: each byte is read
 // and written once (a free: written once).
@@ -24,6 +24,7 @@ constexpr int kMoveThreads = 256;
 constexpr int kVecsPerLane = 8;
 constexpr int kWarpVecs = 32 * kVecsPerLane;  // vectors that a warp moves at a time
 constexpr int kMaxStripBytes = 192 * 1024;
+constexpr int kFewStripBytes = 32 * 1024;  // 128 bytes of each of kMoveThreads pairs
 
 // work layout: [0] number of pairs, [1] whether a destination is another pair's source, then
 // src[n], dst[n], and the plan's own table [max_slots]
@@ -37,23 +38,29 @@ __host__ __device__ __forceinline__ Work work_of(const PoolArgs& a, int32_t cap)
   return {a.work, a.work + 4, a.work + 4 + cap, a.work + 4 + 2 * (size_t)cap};
 }
 
-// exclusive rank of `flag` among the CTA's threads, and the total, through warp ballots
-__device__ __forceinline__ int block_rank(bool flag, int* s_warp, int& total) {
+// Exclusive prefix sums of one number per thread, and the total.
+__device__ __forceinline__ int block_prefix(int x, int* s_warp, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned m = __ballot_sync(0xffffffffu, flag);
-  if (lane == 0) s_warp[warp] = __popc(m);
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll 8
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    const int c = s_warp[w];
-    before += w < warp ? c : 0;
-    all += c;
+  int sum = x;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
   }
+  if (lane == 31) s_warp[warp] = sum;
   __syncthreads();
-  total = all;
-  return before + __popc(m & ((1u << lane) - 1));
+  int w = s_warp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  __syncthreads();  // s_warp may be written again
+  return (warp > 0 ? before : 0) + sum - x;
 }
+static_assert(kPlanThreads == 1024, "block_prefix adds up 32 warps");
 
 __device__ void plan_copy(const PoolArgs& a, const Work w) {
   __shared__ int s_count, s_hazard;
@@ -94,19 +101,34 @@ __device__ void plan_copy(const PoolArgs& a, const Work w) {
   }
 }
 
+// Slots are dealt to the threads in runs of equal length, so that one prefix sum over the runs' counts
+// gives every slot its number of live slots before it, and with it every rank that a plan needs.
+struct Run {
+  int first, end;
+};
+__device__ __forceinline__ Run run_of(int slots) {
+  const int each = (slots + kPlanThreads - 1) / kPlanThreads;
+  const int first = min((int)threadIdx.x * each, slots);
+  return {first, min(first + each, slots)};
+}
+__device__ __forceinline__ int count_live(const int32_t* live, Run run) {
+  int n = 0;
+  for (int s = run.first; s < run.end; ++s) n += live[s] != 0;
+  return n;
+}
+
 __device__ void plan_fork(const PoolArgs& a, const Work w) {
   __shared__ int s_warp[kPlanThreads / 32];
   // the free slots, lowest first, as many as the list can ask for
-  int free_slots = 0;
-  for (int base = 0; base < a.max_slots && free_slots < a.n; base += kPlanThreads) {
-    const int s = base + threadIdx.x;
-    const bool f = s < a.max_slots && a.live[s] == 0;
-    int total;
-    const int r = free_slots + block_rank(f, s_warp, total);
-    if (f && r < a.n) w.table[r] = s;
-    free_slots += total;
+  const Run run = run_of(a.max_slots);
+  int live;
+  int before = block_prefix(count_live(a.live, run), s_warp, live);
+  for (int s = run.first; s < run.end; ++s) {
+    const bool l = a.live[s] != 0;
+    if (!l && s - before < a.n) w.table[s - before] = s;
+    before += l;
   }
-  if (free_slots > a.n) free_slots = a.n;
+  const int free_slots = min(a.max_slots - live, a.n);
   __syncthreads();
   int asked = 0;
   for (int base = 0; base < a.n; base += kPlanThreads) {
@@ -114,7 +136,7 @@ __device__ void plan_fork(const PoolArgs& a, const Work w) {
     const int32_t s = i < a.n ? a.src[i] : -1;
     const bool ok = s >= 0 && s < a.max_slots && a.live[s] != 0;
     int total;
-    const int r = asked + block_rank(ok, s_warp, total);
+    const int r = asked + block_prefix(ok, s_warp, total);
     if (i < a.n) {
       const bool got = ok && r < free_slots;
       const int32_t d = got ? w.table[r] : -1;
@@ -158,41 +180,35 @@ __device__ void plan_free(const PoolArgs& a, const Work w) {
 
 __device__ void plan_compact(const PoolArgs& a, const Work w) {
   __shared__ int s_warp[kPlanThreads / 32];
-  __shared__ int s_live;
-  if (threadIdx.x == 0) s_live = 0;
+  __shared__ int s_kept;
+  const Run run = run_of(a.max_slots);
+  int live;
+  const int first = block_prefix(count_live(a.live, run), s_warp, live);
+  if (live == a.max_slots) {
+    if (threadIdx.x == 0) s_kept = live;
+  } else if (run.first <= live && live < run.end) {  // live slots that stay: those below the number of live ones
+    int before = first;
+    for (int s = run.first; s < live; ++s) before += a.live[s] != 0;
+    s_kept = before;
+  }
   __syncthreads();
-  int mine = 0;
-  for (int s = threadIdx.x; s < a.max_slots; s += kPlanThreads) mine += a.live[s] != 0;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&s_live, mine);
-  __syncthreads();
-  const int live = s_live;
-  int holes = 0, movers = 0;
-  for (int base = 0; base < a.max_slots; base += kPlanThreads) {
-    const int s = base + threadIdx.x;
-    const bool l = s < a.max_slots && a.live[s] != 0;
-    int total;
-    const bool hole = s < live && !l, mover = s >= live && l;
-    if (base < live) {
-      const int r = holes + block_rank(hole, s_warp, total);
-      if (hole) w.dst[r] = s;
-      holes += total;
-    }
-    if (base + kPlanThreads > live) {
-      const int r = movers + block_rank(mover, s_warp, total);
-      if (mover) w.src[r] = s;
-      movers += total;
-    }
-    if (s < a.max_slots) w.table[s] = l ? s : -1;
+  const int kept = s_kept, holes = live - kept;
+  int before = first;
+  for (int s = run.first; s < run.end; ++s) {
+    const bool l = a.live[s] != 0;
+    if (s < live && !l) w.dst[s - before] = s;
+    if (s >= live && l) w.src[before - kept] = s;
+    w.table[s] = l ? s : -1;
+    a.live[s] = s < live;
+    before += l;
   }
   __syncthreads();
   for (int r = threadIdx.x; r < holes; r += kPlanThreads) w.table[w.src[r]] = w.dst[r];
-  for (int s = threadIdx.x; s < a.max_slots; s += kPlanThreads) a.live[s] = s < live;
   __syncthreads();
   for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
     const int32_t s = a.indices[i];
-    if (s >= 0 && s < a.max_slots && w.table[s] >= 0) a.indices[i] = w.table[s];
+    const int32_t to = s >= 0 && s < a.max_slots ? w.table[s] : -1;
+    if (to >= 0) a.indices[i] = to;
     else if (s != -1) report(a.status, KDA_ERR_DEVICE_CHECK);  // no live slot: left as it is
   }
   if (threadIdx.x == 0) {
@@ -203,6 +219,7 @@ __device__ void plan_compact(const PoolArgs& a, const Work w) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) pool_plan_kernel(const PoolArgs a, const Work w, const PoolOp op) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the move may take its place on the SMs
   if (op == kPoolCopy) plan_copy(a, w);
   else if (op == kPoolFork) plan_fork(a, w);
   else if (op == kPoolFree) plan_free(a, w);
@@ -268,10 +285,56 @@ __device__ void move_strips(const PoolArgs& a, const Work& w, int m, int smem_by
 template <typename V, PoolOp kOp>
 __global__ void __launch_bounds__(kMoveThreads) pool_move_kernel(const PoolArgs a, const Work w, int smem_bytes) {
   extern __shared__ __align__(16) unsigned char buf[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
   const int m = w.head[0];
   if (m == 0) return;
   if (kOp == kPoolCopy && w.head[1]) move_strips<V>(a, w, m, smem_bytes, reinterpret_cast<V*>(buf));
   else move_flat<V, kOp == kPoolFree>(a, w, m);
+}
+
+// A copy of at most kMoveThreads pairs in one launch: every CTA works out the plan itself, a thread per
+// pair, in as many steps as there are pairs.
+template <typename V>
+__global__ void __launch_bounds__(kMoveThreads) pool_copy_few_kernel(const PoolArgs a, int smem_bytes) {
+  extern __shared__ __align__(16) unsigned char buf[];
+  __shared__ int32_t s_src[kMoveThreads], s_dst[kMoveThreads], s_from[kMoveThreads], s_to[kMoveThreads];
+  __shared__ int s_taken[kMoveThreads / 32];
+  const int i = threadIdx.x;
+  int32_t s = -1, d = -1;
+  if (i < a.n) {
+    s = a.src[i];
+    d = a.dst[i];
+  }
+  bool ok = s >= 0 && s < a.max_slots && d >= 0 && d < a.max_slots;
+  bool wrong = !ok && (s != -1 || d != -1);
+  s_src[i] = ok ? s : -1;
+  s_dst[i] = ok ? d : -1;
+  __syncthreads();
+  bool named = false;
+  for (int j = 0; j < i && j < a.n; ++j) named |= ok && s_dst[j] == d;
+  wrong |= named;  // a destination named twice: the first pair counts
+  ok = ok && !named && s != d;
+  if (blockIdx.x == 0 && wrong) report(a.status, KDA_ERR_DEVICE_CHECK);
+  bool over = false;  // whether another pair writes this pair's source
+  for (int j = 0; j < a.n; ++j) over |= s_dst[j] == s && s_src[j] != s;
+  // the pairs that count, in the list's order: all CTAs share the work by their place in it
+  const unsigned taken = __ballot_sync(0xffffffffu, ok);
+  if ((i & 31) == 0) s_taken[i >> 5] = __popc(taken);
+  const bool hazard = __syncthreads_or(ok && over);
+  int m = 0, at = __popc(taken & ((1u << (i & 31)) - 1));
+  for (int k = 0; k < kMoveThreads / 32; ++k) {
+    at += k < i >> 5 ? s_taken[k] : 0;
+    m += s_taken[k];
+  }
+  if (ok) {
+    s_from[at] = s;
+    s_to[at] = d;
+  }
+  __syncthreads();
+  const Work w{nullptr, s_from, s_to, nullptr};
+  if (m == 0) return;
+  if (hazard) move_strips<V>(a, w, m, smem_bytes, reinterpret_cast<V*>(buf));
+  else move_flat<V, false>(a, w, m);
 }
 
 template <typename V>
@@ -284,22 +347,38 @@ cudaError_t launch_move(const PoolArgs& a, const Work& w, PoolOp op, int32_t cap
   const int64_t units = (vecs + kWarpVecs - 1) / kWarpVecs * cap * a.layers;
   const int64_t ctas = (units + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
   const unsigned grid = (unsigned)(ctas < 8 * sms ? ctas : 8 * sms);
+  if (op == kPoolCopy && a.n <= kMoveThreads) {
+    pool_copy_few_kernel<V><<<grid, kMoveThreads, kFewStripBytes, stream>>>(a, kFewStripBytes);
+    return cudaGetLastError();
+  }
+  pool_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, w, op);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   int smem = 0;
   void (*kernel)(const PoolArgs, const Work, int);
   if (op == kPoolCopy) {
-    // a strip of 128 bytes of every pair where that fits 48 KB (four CTAs per SM), else narrower ones
+    // a strip of 128 bytes of every pair where that fits, else narrower ones
     const int64_t want = (int64_t)cap * 128;
-    smem = want <= 48 * 1024 ? 48 * 1024 : want < kMaxStripBytes ? (int)want : kMaxStripBytes;
+    smem = want < kMaxStripBytes ? (int)want : kMaxStripBytes;
     kernel = pool_move_kernel<V, kPoolCopy>;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStripBytes);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStripBytes);
   } else if (op == kPoolFree) {
     kernel = pool_move_kernel<V, kPoolFree>;
   } else {
     kernel = pool_move_kernel<V, kPoolFork>;
   }
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kMoveThreads, smem, stream>>>(a, w, smem);
-  return cudaGetLastError();
+  // the move's launch overlaps the plan; it waits for the plan's end itself
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, w, smem);
 }
 
 // entries of the pair lists: what one call can move at most
@@ -311,15 +390,15 @@ int32_t list_size(int32_t n, int32_t max_slots, PoolOp op) {
 }  // namespace
 
 size_t pool_work_ints(int32_t n, int32_t max_slots) {
-  return 4 + 2 * (size_t)(n > max_slots ? n : max_slots) + (size_t)(n > max_slots ? n : max_slots);
+  const size_t most = n > max_slots ? n : max_slots;
+  return 4 + 3 * most;
 }
+
+bool pool_needs_work(PoolOp op, int32_t n) { return op != kPoolCopy || n > kMoveThreads; }
 
 cudaError_t launch_pool(const PoolArgs& a, PoolOp op, cudaStream_t stream) {
   const int32_t cap = list_size(a.n, a.max_slots, op);
   const Work w = work_of(a, a.n > a.max_slots ? a.n : a.max_slots);
-  pool_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, w, op);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   const bool vec = a.slot_elems % 4 == 0 && (reinterpret_cast<uintptr_t>(a.pool) & 15u) == 0;
   return vec ? launch_move<uint4>(a, w, op, cap, stream) : launch_move<uint32_t>(a, w, op, cap, stream);
 }

@@ -17,15 +17,14 @@
 //     fragments.  Every fp32 factor is split into two bf16 parts and three of the four partial
 //     products are summed (2^-18 of the factors is lost): kda_tree_commit writes the results of this
 //     into fp32 states, which one bf16 product would spoil.
-//  3. each value column's thread solves down the tree, then the outputs follow.
+//  3. blocks of 16 nodes down the tree: a product with the deltas of the blocks before, then a thread per
+//     value column substitutes within the block; a last product gives the outputs.
 // It is bound by the state's 4 dk dv bytes for drafts of about 16 nodes and fewer.  tcgen05 is not
 // used: with 2 N <= 128 rows against a 128 x 128 state read once, staging S through shared memory
 // for it costs more than the whole product does here.
 //
 // The commit is S' = e^{G_a} o S + sum over the path (k_j o e^{G_a - G_j}) u_j^T, one pass over the
 // state, bound by its 8 dk dv bytes.
-#include <type_traits>
-
 #include "kda_glr_math.cuh"
 #include "kda_ops_internal.h"
 #include "kda_sm100.cuh"
@@ -38,12 +37,17 @@ constexpr int kPitch = 132;    // floats of a node's row in shared memory
 constexpr uint64_t kWaitNs = 1000000000ull;  // limit of the wait for a copy
 constexpr int kPitchH = 144;   // bf16 of a row of the split factors (32 bytes past 256: no conflicts)
 
-// Offsets, slot and parents of a sequence; false where one is out of range.  All threads call it.
-__device__ __forceinline__ bool tree_of(const TreeArgs& a, int b, int32_t& m0, int32_t& n, int32_t& slot, int32_t* s_par) {
+// Offsets and slot of a sequence; false where one is out of range.
+__device__ __forceinline__ bool tree_at(const TreeArgs& a, int b, int32_t& m0, int32_t& n, int32_t& slot) {
   m0 = a.cu[b];
   n = a.cu[b + 1] - m0;
   slot = a.slots[b];
-  bool ok = m0 >= 0 && n >= 0 && n <= a.max_nodes && (int64_t)m0 + n <= a.total_nodes && slot >= 0 && slot < a.max_slots;
+  return m0 >= 0 && n >= 0 && n <= a.max_nodes && (int64_t)m0 + n <= a.total_nodes && slot >= 0 && slot < a.max_slots;
+}
+
+// The same with the parents, which go to shared memory.  All threads call it.
+__device__ __forceinline__ bool tree_of(const TreeArgs& a, int b, int32_t& m0, int32_t& n, int32_t& slot, int32_t* s_par) {
+  bool ok = tree_at(a, b, m0, n, slot);
   if (ok && (int)threadIdx.x < n) {
     const int32_t par = a.parents[m0 + threadIdx.x];
     s_par[threadIdx.x] = par;
@@ -74,7 +78,7 @@ struct TreeSmem {
   union {
     alignas(128) float state[128 * 128];
     struct {
-      float u[kNodes][128], qs[kNodes][128];
+      float u[kNodes < 16 ? 16 : kNodes][128], qs[kNodes < 16 ? 16 : kNodes][128];
     };
   };
   // keys and decays (1), then the factors of the product with the state (2).  Factor rows 16 t + r:
@@ -87,7 +91,10 @@ struct TreeSmem {
       __nv_bfloat16 hi[2 * kNodes][kPitchH], lo[2 * kNodes][kPitchH];
     };
   };
-  float a[kNodes][kNodes + 4], b[kNodes][kNodes + 4];  // zero where j is no ancestor of i
+  // scores, zero where j is no ancestor of i; the pitch keeps 16-byte reads of neighbouring rows apart
+  static constexpr int kRows = kNodes < 16 ? 16 : kNodes;
+  static constexpr int kPitchS = kRows + (kNodes == 64 ? 16 : 4);
+  float a[kRows][kPitchS], b[kRows][kPitchS];
   float beta[kNodes];
   int32_t par[kNodes];
   uint64_t full;
@@ -109,39 +116,33 @@ __device__ __forceinline__ float4 load_quad(const T* row, int c, int d) {
   }
 }
 
-// the sum over j < kCount of row[j] u[j], in four chains
-template <int kCount>
-__device__ __forceinline__ float dot(const float* row, const float* u) {
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < kCount; j += 4) {
-    const float4 w = *reinterpret_cast<const float4*>(row + j);
-    s[0] = fmaf(w.x, u[j], s[0]);
-    s[1] = fmaf(w.y, u[j + 1], s[1]);
-    s[2] = fmaf(w.z, u[j + 2], s[2]);
-    s[3] = fmaf(w.w, u[j + 3], s[3]);
-  }
-  return (s[0] + s[1]) + (s[2] + s[3]);
-}
-
-// Blocks of kBlk nodes, one after the other (a loop that the compiler unrolls, since u sits in registers).
-template <int kNodes, int kBlk, int kFirst, typename F>
-__device__ __forceinline__ void each_block(F&& f) {
-  if constexpr (kFirst < kNodes) {
-    f(std::integral_constant<int, kFirst>{});
-    each_block<kNodes, kBlk, kFirst + kBlk>(f);
-  }
+// The fragments of a 16 x 16 tile of scores in two bf16 parts (rows from smem, the summed index permuted
+// as in the product with the state)
+__device__ __forceinline__ void split_scores(const float* row0, const float* row8, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  const float4 x = *reinterpret_cast<const float4*>(row0), y = *reinterpret_cast<const float4*>(row8);
+  split2(x.x, x.y, hi[0], lo[0]);
+  split2(y.x, y.y, hi[1], lo[1]);
+  split2(x.z, x.w, hi[2], lo[2]);
+  split2(y.z, y.w, hi[3], lo[3]);
 }
 
 template <int kNodes, bool kVFirst, bool kFull, typename T>
-__global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(const TreeArgs p) {
+__global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(const TreeArgs p, const bool wide_out) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   TreeSmem<kNodes>& sm = *reinterpret_cast<TreeSmem<kNodes>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv, kh = h / (p.Hv / p.Hk);
   const int dk = kFull ? 128 : p.dk, dv = kFull ? 128 : p.dv;
+  // every load of the nodes is on its way before the first one is waited for
+  const int c4 = 4 * lane;
+  const float a_log = p.a_log[h];
+  const float4 bias = load_quad<kFull>(p.dt_bias + (size_t)h * dk, c4, dk);
   int32_t m0, n, slot;
-  if (!tree_of(p, b, m0, n, slot, sm.par)) return;
+  const bool there = tree_at(p, b, m0, n, slot);
+  if (!there) {
+    if (tid == 0) report(p.status, KDA_ERR_DEVICE_CHECK);
+    return;
+  }
   if (n == 0) return;
   const float* state = p.pool + ((size_t)slot * p.Hv + h) * (size_t)dk * dv;
   if constexpr (kFull) {  // the state comes while the scores are worked out
@@ -153,59 +154,69 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
       sm100::bulk_g2s(sm100::smem_addr(sm.state), state, sizeof(sm.state), bar);
     }
   }
-
-  // ---- keys, decays and beta of all nodes (zero keys past dk); no scores yet
   const T* qs = reinterpret_cast<const T*>(p.q) + ((size_t)m0 * p.Hk + kh) * dk;
   const T* ks = reinterpret_cast<const T*>(p.k) + ((size_t)m0 * p.Hk + kh) * dk;
   const float* raws = p.raw_gate + ((size_t)m0 * p.Hv + h) * dk;
   const size_t k_row = (size_t)p.Hk * dk, raw_row = (size_t)p.Hv * dk;
-  {
-    const glr::HeadGate gate = glr::head_gate(p.a_log[h], p.flags & KDA_GATE_SAFE, p.lb);
-    const int c = 4 * (tid & 31);
-    const float4 bias = load_quad<kFull>(p.dt_bias + (size_t)h * dk, c, dk);
-    const float2 bias0 = glr::mul2(make_float2(bias.x, bias.y), glr::both(glr::kLog2e));
-    const float2 bias1 = glr::mul2(make_float2(bias.z, bias.w), glr::both(glr::kLog2e));
-    constexpr int kAtOnce = kNodes >= 32 ? 4 : kNodes / 8;  // rows of a warp with their loads in flight together
-#pragma unroll 1
-    for (int m1 = warp; m1 < n; m1 += 8 * kAtOnce) {
-      float4 kv[kAtOnce], raw[kAtOnce];
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int m = min(m1 + 8 * j, n - 1);
-        kv[j] = load_quad<kFull>(ks + m * k_row, c, dk);
-        raw[j] = load_quad<kFull>(raws + m * raw_row, c, dk);
-      }
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int m = m1 + 8 * j;
-        if (m < n) {
-          const float2 z0 = glr::pre_log2(make_float2(raw[j].x, raw[j].y), bias0);
-          const float2 z1 = glr::pre_log2(make_float2(raw[j].z, raw[j].w), bias1);
-          const float2 g0 = glr::clamp2(glr::gate_log2(z0, glr::exp_neg_abs(z0), gate.c), gate.lb2);
-          const float2 g1 = glr::clamp2(glr::gate_log2(z1, glr::exp_neg_abs(z1), gate.c), gate.lb2);
-          *reinterpret_cast<float4*>(&sm.k[m][c]) = kv[j];
-          *reinterpret_cast<float4*>(&sm.al[m][c]) = make_float4(glr::ex2(g0.x), glr::ex2(g0.y), glr::ex2(g1.x), glr::ex2(g1.y));
-        }
-      }
-    }
-    for (int i = tid; i < kNodes * (kNodes + 4) / 4; i += kThreads) {
-      reinterpret_cast<float4*>(sm.a)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      reinterpret_cast<float4*>(sm.b)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    for (int m = tid; m < n; m += kThreads)
-      sm.beta[m] = beta_f32(p.beta[(size_t)(m0 + m) * p.Hv + h], p.flags & KDA_BETA_PROB);
-  }
   constexpr int kGroup = kThreads / kNodes;  // lanes per node
   constexpr int kQuads = 32 / kGroup;        // float4's of channels per lane
   static_assert(kGroup <= 32 && kQuads >= 1, "");
+  constexpr int kAtOnce = kNodes >= 32 ? 4 : kNodes / 8;  // rows of a warp with their loads in flight together
   const int node = tid / kGroup, g = tid % kGroup;
-  float4 qq[kQuads];
+  const int mine = min(tid, n - 1);
+  const int32_t parent = p.parents[m0 + mine];
+  const float beta = p.beta[(size_t)(m0 + mine) * p.Hv + h];
+  float4 kv[kAtOnce], raw[kAtOnce], qq[kQuads];
+  auto load_rows = [&](int m1) {
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int m = min(m1 + 8 * j, n - 1);
+      kv[j] = load_quad<kFull>(ks + m * k_row, c4, dk);
+      raw[j] = load_quad<kFull>(raws + m * raw_row, c4, dk);
+    }
+  };
+  load_rows(warp);
 #pragma unroll
   for (int j = 0; j < kQuads; ++j) {
     qq[j] = load_quad<kFull>(qs + min(node, n - 1) * k_row, 4 * (g + kGroup * j), dk);
     if (node >= n) qq[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  __syncthreads();
+  for (int i = tid; i < (int)(sizeof(sm.a) + sizeof(sm.b)) / 16; i += kThreads)
+    reinterpret_cast<float4*>(sm.a)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  // ---- keys, decays and beta of all nodes (zero keys past dk); no scores yet
+  if (tid < kNodes) {
+    sm.par[tid] = parent;
+    sm.beta[tid] = tid < n ? beta_f32(beta, p.flags & KDA_BETA_PROB) : 0.f;
+  }
+  {
+    const glr::HeadGate gate = glr::head_gate(a_log, p.flags & KDA_GATE_SAFE, p.lb);
+    const float2 bias0 = glr::mul2(make_float2(bias.x, bias.y), glr::both(glr::kLog2e));
+    const float2 bias1 = glr::mul2(make_float2(bias.z, bias.w), glr::both(glr::kLog2e));
+#pragma unroll 1
+    for (int m1 = warp; m1 < n; m1 += 8 * kAtOnce) {
+      if (m1 != warp) load_rows(m1);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int m = m1 + 8 * j;
+        const float2 z0 = glr::pre_log2(make_float2(raw[j].x, raw[j].y), bias0);
+        const float2 z1 = glr::pre_log2(make_float2(raw[j].z, raw[j].w), bias1);
+        const float2 g0 = glr::clamp2(glr::gate_log2(z0, glr::exp_neg_abs(z0), gate.c), gate.lb2);
+        const float2 g1 = glr::clamp2(glr::gate_log2(z1, glr::exp_neg_abs(z1), gate.c), gate.lb2);
+        if (m < n) {
+          *reinterpret_cast<float4*>(&sm.k[m][c4]) = kv[j];
+          *reinterpret_cast<float4*>(&sm.al[m][c4]) = make_float4(glr::ex2(g0.x), glr::ex2(g0.y), glr::ex2(g1.x), glr::ex2(g1.y));
+        }
+      }
+    }
+  }
+  if (!__syncthreads_and(parent >= -1 && parent < mine)) {
+    if constexpr (kFull) {  // the copy in flight writes to this CTA's memory
+      if (!sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    }
+    if (tid == 0) report(p.status, KDA_ERR_DEVICE_CHECK);
+    return;
+  }
 
   // ---- 1. scores, and the factors of the product with the state
   {
@@ -270,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
     if (!sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
   }
   {
-    const int q = lane & 3, gr = lane >> 2, col = 16 * warp + 2 * gr;
+    const int q = lane & 3, gr = lane >> 2, col = 16 * warp + 2 * gr;  // a lane's first column of S
     uint32_t bh[8][2][2], bl[8][2][2];  // [k-step][n-tile][register]
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
@@ -330,80 +341,140 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
   }
   __syncthreads();
 
-  // ---- 3. down the tree, a thread per value column and block by block: one half of the CTA solves a
-  // block of nodes while the other half works out the outputs of the block before it.  The sums run
-  // over all earlier nodes, weights being zero where one is no ancestor; a delta that is not finite
-  // must not reach other branches through such a zero, so from the first one on, ancestors are walked.
-  constexpr int kBlk = kNodes < 16 ? kNodes : 16;
-  const int col = tid & 127;
-  const bool solving = tid < 128, mine = col < dv;
-  bool walk = false;
-  float u[kNodes];
+  // ---- 3. down the tree, 16 nodes at a time: what earlier blocks contribute is a matrix product (split
+  // as above), the rest a substitution with a thread per value column.  The products run over all
+  // nodes, weights being zero where one is no ancestor; a delta that is not finite must not reach
+  // other branches through such a zero, so from the first one on, ancestors are walked instead.
+  const int q = lane & 3, gr = lane >> 2, c0 = 16 * warp + 4 * q;  // a lane's columns of the products
+  const int blocks = (n + 15) >> 4, col = tid & 127;
   const size_t row = (size_t)p.Hv * dv;
-  const T* vs = reinterpret_cast<const T*>(p.v) + ((size_t)m0 * p.Hv + h) * dv + (mine ? col : 0);
-  each_block<kNodes, kBlk, 0>([&](auto first) {
-    constexpr int i0 = decltype(first)::value;
-    if (i0 >= n) return;
-    const int end = min(n, i0 + kBlk);
-    const size_t at = ((size_t)(m0 + i0) * p.Hv + h) * dv + col;
+  const T* vs = reinterpret_cast<const T*>(p.v) + ((size_t)m0 * p.Hv + h) * dv;
+  float* deltas = p.deltas + ((size_t)m0 * p.Hv + h) * dv;
+  bool walk = false;
+  constexpr int kBlocks = (kNodes + 15) / 16;
+  uint32_t uh[kBlocks][2][2], ul[kBlocks][2][2];  // solved blocks as fragments: [block][n-tile][register]
+  float4 v0 = load_quad<kFull>(vs + min(gr, n - 1) * row, c0, dv), v8 = load_quad<kFull>(vs + min(gr + 8, n - 1) * row, c0, dv);
+#pragma unroll
+  for (int blk = 0; blk < kBlocks; ++blk) {
+    if (blk >= blocks) break;
+    const int i0 = 16 * blk;
+    {
+      float big[2][4] = {}, small[2][4] = {};
+#pragma unroll
+      for (int kb = 0; kb < blk; ++kb) {
+        uint32_t ah[4], al[4];
+        split_scores(&sm.a[i0 + gr][16 * kb + 4 * q], &sm.a[i0 + gr + 8][16 * kb + 4 * q], ah, al);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          mma_bf16(big[nt], ah, uh[kb][nt][0], uh[kb][nt][1]);
+          mma_bf16(small[nt], al, uh[kb][nt][0], uh[kb][nt][1]);
+          mma_bf16(small[nt], ah, ul[kb][nt][0], ul[kb][nt][1]);
+        }
+      }
+      float4* r0 = reinterpret_cast<float4*>(&sm.u[i0 + gr][c0]);
+      float4* r8 = reinterpret_cast<float4*>(&sm.u[i0 + gr + 8][c0]);
+      const float4 x = *r0, y = *r8;
+      auto part = [&](int nt, int e) { return walk ? 0.f : big[nt][e] + small[nt][e]; };
+      *r0 = make_float4(v0.x - x.x - part(0, 0), v0.y - x.y - part(1, 0), v0.z - x.z - part(0, 1), v0.w - x.w - part(1, 1));
+      if (kNodes >= 16)
+        *r8 = make_float4(v8.x - y.x - part(0, 2), v8.y - y.y - part(1, 2), v8.z - y.z - part(0, 3), v8.w - y.w - part(1, 3));
+    }
+    if (blk + 1 < blocks) {
+      v0 = load_quad<kFull>(vs + min(i0 + 16 + gr, n - 1) * row, c0, dv);
+      v8 = load_quad<kFull>(vs + min(i0 + 24 + gr, n - 1) * row, c0, dv);
+    }
+    __syncthreads();
     bool odd = false;
-    if (solving) {
-      float v[kBlk];
+    constexpr int kIn = kNodes < 16 ? kNodes : 16;
+    float r[kIn];
+    if (tid < 128) {
 #pragma unroll
-      for (int i = 0; i < kBlk; ++i) v[i] = glr::to_f32(vs[min(i0 + i, n - 1) * row]);
+      for (int i = 0; i < kIn; ++i) r[i] = i0 + i < n ? sm.u[i0 + i][col] : 0.f;
 #pragma unroll
-      for (int i = 0; i < kBlk; ++i) v[i] = i0 + i < n && mine ? v[i] - sm.u[i0 + i][col] : 0.f;
+      for (int j = 0; j < kIn; ++j) {
+        r[j] *= sm.beta[i0 + j];
+        odd |= !isfinite(r[j]);
 #pragma unroll
-      for (int i = 0; i < kBlk; ++i) {
-        float r = v[i];
-        if (i0 > 0) r -= dot<i0>(sm.a[i0 + i], u);
-#pragma unroll
-        for (int j = 0; j < i; ++j) r = fmaf(-sm.a[i0 + i][i0 + j], u[i0 + j], r);
-        u[i0 + i] = i0 + i < n ? r * sm.beta[i0 + i] : 0.f;
-        odd |= !isfinite(u[i0 + i]);
+        for (int i = j + 1; i < kIn; ++i) r[i] = fmaf(-sm.a[i0 + i][i0 + j], r[j], r[i]);
       }
     }
-    walk |= __syncthreads_or(odd) != 0;
-    if (solving && mine) {
+    // (what other columns of a row past dv hold is nobody's)
+    const bool before = walk;
+    walk |= __syncthreads_or(odd && col < dv) != 0;
+    if (tid < 128) {
       if (!walk) {
 #pragma unroll
-        for (int i = 0; i < kBlk; ++i) {
-          if (i0 + i < n) {
-            sm.u[i0 + i][col] = u[i0 + i];
-            p.deltas[at + i * row] = u[i0 + i];
-          }
+        for (int i = 0; i < kIn; ++i) {
+          sm.u[i0 + i][col] = r[i];
+          if (i0 + i < n && col < dv) deltas[(i0 + i) * row + col] = r[i];
         }
       } else {
-        for (int i = i0; i < end; ++i) {
-          float r = glr::to_f32(vs[i * row]) - sm.u[i][col];
-          for (int j = sm.par[i]; j >= 0; j = sm.par[j]) r = fmaf(-sm.a[i][j], sm.u[j][col], r);
-          r *= sm.beta[i];
-          sm.u[i][col] = r;
-          p.deltas[at + (i - i0) * row] = r;
+        for (int i = i0; i < min(i0 + 16, n); ++i) {
+          float s = sm.u[i][col];
+          for (int j = sm.par[i]; j >= (before ? 0 : i0); j = sm.par[j]) s = fmaf(-sm.a[i][j], sm.u[j][col], s);
+          s *= sm.beta[i];
+          sm.u[i][col] = s;
+          if (col < dv) deltas[i * row + col] = s;
         }
       }
     }
     __syncthreads();
-    if (!solving && mine) {
-      if (!walk) {
+    if (!walk) {
+      const int i = i0 + 4 * q, cc = 16 * warp + 2 * gr;
+      float2 w[4];
 #pragma unroll
-        for (int i = 0; i < kBlk; ++i) u[i0 + i] = i0 + i < n ? sm.u[i0 + i][col] : 0.f;
-#pragma unroll 4
-        for (int i = 0; i < kBlk; ++i) {
-          if (i0 + i < n) {
-            const float r = sm.qs[i0 + i][col] + dot<i0 + kBlk>(sm.b[i0 + i], u);
-            store_out(p.out, at + i * row, r, p.out_bf16);
-          }
+      for (int e = 0; e < 4; ++e) w[e] = kNodes >= 16 || 4 * q + e < kNodes ? *reinterpret_cast<const float2*>(&sm.u[i + e][cc]) : make_float2(0.f, 0.f);
+      split2(w[0].x, w[1].x, uh[blk][0][0], ul[blk][0][0]);
+      split2(w[2].x, w[3].x, uh[blk][0][1], ul[blk][0][1]);
+      split2(w[0].y, w[1].y, uh[blk][1][0], ul[blk][1][0]);
+      split2(w[2].y, w[3].y, uh[blk][1][1], ul[blk][1][1]);
+    }
+  }
+  // ---- outputs: (Q o e^G) S plus the scores' product with the deltas
+  if (!walk) {
+#pragma unroll
+    for (int blk = 0; blk < kBlocks; ++blk) {
+      if (blk >= blocks) break;
+      const int i0 = 16 * blk;
+      float big[2][4] = {}, small[2][4] = {};
+#pragma unroll
+      for (int kb = 0; kb <= blk; ++kb) {
+        uint32_t bh[4], bl[4];
+        split_scores(&sm.b[i0 + gr][16 * kb + 4 * q], &sm.b[i0 + gr + 8][16 * kb + 4 * q], bh, bl);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          mma_bf16(big[nt], bh, uh[kb][nt][0], uh[kb][nt][1]);
+          mma_bf16(small[nt], bl, uh[kb][nt][0], uh[kb][nt][1]);
+          mma_bf16(small[nt], bh, ul[kb][nt][0], ul[kb][nt][1]);
         }
-      } else {
-        for (int i = i0; i < end; ++i) {
-          float r = sm.qs[i][col];
-          for (int j = i; j >= 0; j = sm.par[j]) r = fmaf(sm.b[i][j], sm.u[j][col], r);
-          store_out(p.out, at + (i - i0) * row, r, p.out_bf16);
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int i = i0 + gr + 8 * half;
+        if (i < n) {
+          const float4 x = *reinterpret_cast<const float4*>(&sm.qs[i][c0]);
+          const float o[4] = {x.x + big[0][2 * half] + small[0][2 * half], x.y + big[1][2 * half] + small[1][2 * half],
+                              x.z + big[0][2 * half + 1] + small[0][2 * half + 1],
+                              x.w + big[1][2 * half + 1] + small[1][2 * half + 1]};
+          const size_t at = ((size_t)(m0 + i) * p.Hv + h) * dv + c0;
+          if (kFull && wide_out) {
+            if (p.out_bf16) glr::store4(reinterpret_cast<__nv_bfloat16*>(p.out) + at, make_float2(o[0], o[1]), make_float2(o[2], o[3]));
+            else glr::store4(reinterpret_cast<float*>(p.out) + at, make_float2(o[0], o[1]), make_float2(o[2], o[3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (c0 + e < dv) store_out(p.out, at + e, o[e], p.out_bf16);
+          }
         }
       }
     }
-  });
+  } else if (col < dv) {
+    for (int i = tid >> 7; i < n; i += kThreads / 128) {
+      float s = sm.qs[i][col];
+      for (int j = i; j >= 0; j = sm.par[j]) s = fmaf(sm.b[i][j], sm.u[j][col], s);
+      store_out(p.out, ((size_t)(m0 + i) * p.Hv + h) * dv + col, s, p.out_bf16);
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------------ commit
@@ -508,13 +579,13 @@ __global__ void __launch_bounds__(kThreads, 2) commit_kernel(const TreeArgs p) {
   }
 }
 
-template <typename Kernel>
-cudaError_t launch(Kernel kernel, const TreeArgs& a, size_t smem, cudaStream_t stream) {
+template <typename Kernel, typename... More>
+cudaError_t launch(Kernel kernel, const TreeArgs& a, size_t smem, cudaStream_t stream, More... more) {
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)((int64_t)a.batch * a.Hv), kThreads, smem, stream>>>(a);
+  kernel<<<(unsigned)((int64_t)a.batch * a.Hv), kThreads, smem, stream>>>(a, more...);
   return cudaGetLastError();
 }
 
@@ -528,11 +599,12 @@ cudaError_t pick(const TreeArgs& a, cudaStream_t stream) {
     if (a.v_first) return full ? go(commit_kernel<kNodes, true, true>) : go(commit_kernel<kNodes, true, false>);
     return full ? go(commit_kernel<kNodes, false, true>) : go(commit_kernel<kNodes, false, false>);
   } else {
-    auto go = [&](auto kernel) { return launch(kernel, a, smem, stream); };
+    const bool wide_out = on(a.out, a.out_bf16 ? 8 : 16);
+    auto go = [&](auto kernel) { return launch(kernel, a, smem, stream, wide_out); };
     using bf16 = __nv_bfloat16;
     // the form for 128 x 128 states reads rows in wide accesses: all of them start on 16 bytes (bf16: 8)
     const size_t in = a.in_bf16 ? 8 : 16;
-    const bool wide = full && on(a.q, in) && on(a.k, in) && on(a.raw_gate, 16) && on(a.dt_bias, 16);
+    const bool wide = full && on(a.q, in) && on(a.k, in) && on(a.v, in) && on(a.raw_gate, 16) && on(a.dt_bias, 16);
     if (a.in_bf16) {
       if (a.v_first) return wide ? go(tree_kernel<kNodes, true, true, bf16>) : go(tree_kernel<kNodes, true, false, bf16>);
       return wide ? go(tree_kernel<kNodes, false, true, bf16>) : go(tree_kernel<kNodes, false, false, bf16>);

@@ -18,6 +18,7 @@ __all__ = ["kda_pool_copy", "kda_pool_fork", "kda_pool_free", "kda_pool_compact"
            "MAX_POOL_COPIES"]
 
 MAX_POOL_COPIES = 8192  # pairs of one kda_pool_copy
+FEW_COPIES = 256  # up to so many it takes one launch and no workspace
 
 _vp, _i32, _i64, _sz, _int = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
 SIGNATURES = {
@@ -59,13 +60,17 @@ def _call(what, pool, layout, lists, n, results, workspace, device_status, strea
     index, lib = dev.index, load_library()
     status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
     with _on_device(index):
-        if workspace is None:
+        if workspace is None and what == "kda_pool_copy" and n <= FEW_COPIES:
+            at, size = None, 0
+        elif workspace is None:
             workspace = torch.empty(lib.kda_pool_workspace_size(n, slots), dtype=torch.uint8, device=dev)
             made = (*made, workspace)
+            at, size = workspace.data_ptr(), workspace.numel()
         else:
             _dev(workspace, "workspace", torch.uint8, dev)
-        rc = getattr(lib, what)(pool.data_ptr(), layers, slots, elems, *lists, n, *results, workspace.data_ptr(),
-                                workspace.numel(), status, _on_stream(stream, index))
+            at, size = workspace.data_ptr(), workspace.numel()
+        rc = getattr(lib, what)(pool.data_ptr(), layers, slots, elems, *lists, n, *results, at, size, status,
+                                _on_stream(stream, index))
     _used_on(stream, index, *made)
     if rc != 0:
         raise KdaError(rc, what)
