@@ -94,21 +94,14 @@ __device__ __forceinline__ void put4(T* p, int d, int lane, float2 lo, float2 hi
   }
 }
 
-// A warp's affine maps of its lanes' four channels in shared memory: A then B.
+// An affine map h -> a h + b of a lane's four channels.
 struct Map4 {
   float2 a0, a1, b0, b1;
 };
-struct MapRow {
-  float a[kRow], b[kRow];
-};
-__device__ __forceinline__ Map4 read_map(const MapRow& r, int lane) {
-  const float4 a = *reinterpret_cast<const float4*>(r.a + 4 * lane);
-  const float4 b = *reinterpret_cast<const float4*>(r.b + 4 * lane);
-  return {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
-}
-__device__ __forceinline__ void write_map(MapRow& r, int lane, const Map4& m) {
-  *reinterpret_cast<float4*>(r.a + 4 * lane) = make_float4(m.a0.x, m.a0.y, m.a1.x, m.a1.y);
-  *reinterpret_cast<float4*>(r.b + 4 * lane) = make_float4(m.b0.x, m.b0.y, m.b1.x, m.b1.y);
+
+template <int kId, int kThreads>
+__device__ __forceinline__ void named_barrier_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kThreads) : "memory");
 }
 
 // The sequence of this cluster; false (reported) if its offsets or slot are out of range.
@@ -394,31 +387,48 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
 }
 
 // ------------------------------------------------------------------------------------ backward
+//
+// The same division of labour, from the last tile to the first.  A computing warp first works out the
+// gates of a tile and two maps over its tokens: of h forwards and of a D backwards (they share A); the
+// carrying threads fold the former from the kept state that enters the tile and pass the latter through
+// the cluster; then the gradients follow.  Between the two a warp keeps only the gates, in registers,
+// and reads its inputs again from shared memory, where dx and draw_gate take their place and leave by
+// tensor copies.
 
-constexpr int kBwdThreads = 512;
-constexpr int kBwdWarps = kBwdThreads / 32;
+constexpr int kBwdWarps = 16;
 constexpr int kBwdRows = kTile / kBwdWarps;
+constexpr int kBwdThreads = 32 * (kBwdWarps + kCarryWarps);
+
+struct BwdMaps {
+  CUtensorMap x, raw, dout, dx, draw;
+};
 
 template <typename TX, typename TR, typename TO>
 struct BwdSmem {
-  static constexpr int kStages = sizeof(TX) + sizeof(TR) + sizeof(TO) <= 6 ? 3 : 2;
-  static constexpr int kMaxRanks = sizeof(TX) == 4 ? kMaxCluster / 2 : kMaxCluster;  // what fits
-  TX x[kStages][kTile][kRow];
-  TR raw[kStages][kTile][kRow];
-  TO dout[kStages][kTile][kRow];
-  float beta[kStages][kTile];
-  MapRow fwd_map[kBwdWarps];     // of h through a warp's tokens
-  float rev_b[kBwdWarps][kRow];  // of a_t D_t back through them (the same A)
-  MapRow tile_map[2][kMaxRanks];
+  static constexpr int kStages = sizeof(TX) + sizeof(TR) + sizeof(TO) <= 8 ? 3 : 2;
+  // what fits beside the tiles: two sets of maps (a tile's may be there before the last one's are used), and
+  // the maps of so many CTAs
+  static constexpr bool kAhead = sizeof(TX) + sizeof(TR) + sizeof(TO) <= 6;
+  static constexpr int kMaxRanks = kAhead ? kMaxCluster : kMaxCluster / 2;
+  alignas(128) TX x[kStages][kTile * kRow];
+  alignas(128) TR raw[kStages][kTile * kRow];
+  alignas(128) TO dout[kStages][kTile * kRow];
+  static constexpr int kMapBuffers = kAhead ? 2 : 1;
+  float2 map[kMapBuffers][kBwdWarps][kRow];  // (A, B) forwards; then the state before and a D behind a warp's tokens
+  float rev[kMapBuffers][kBwdWarps][kRow];   // B backwards
+  float2 tile_map[2][kMaxRanks][kRow];
+  uint64_t full[kStages], mapped[2], entered[2], tiles_in[2], done[2];
 };
 
 template <typename TX, typename TR, typename TO, bool kNorm>
 __global__ void __launch_bounds__(kBwdThreads, 1)
-    glr_bwd_kernel(const GlrBwdArgs p, const Access how, const bool vec_grad) {
+    glr_bwd_kernel(const GlrBwdArgs p, const __grid_constant__ BwdMaps maps, const Access how, const bool by_copy,
+                   const bool vec_grad) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   using Smem = BwdSmem<TX, TR, TO>;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   constexpr int kStages = Smem::kStages;
+  constexpr bool kAhead = Smem::kAhead;
 
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -426,12 +436,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.d;
 
   // partial sums of the parameters' gradients, one set per (sequence, rank)
-  float* part_bias = p.partial + ((size_t)(b * ranks + rank) * p.H + h) * (d + 1);
+  float* part = p.partial + ((size_t)(b * ranks + rank) * p.H + h) * (d + 1);
   int32_t s0, n;
   const bool ok = sequence(p.cu, b, p.total_tokens, s0, n);
   if (!ok || n == 0) {
     if (!ok && threadIdx.x == 0) report(p.status, KDA_ERR_DEVICE_CHECK);
-    for (int c = threadIdx.x; c <= d; c += kBwdThreads) part_bias[c] = 0.f;
+    for (int c = threadIdx.x; c <= d; c += kBwdThreads) part[c] = 0.f;
     if (ok && rank == 0)  // the state only passes through an empty sequence
       for (int c = threadIdx.x; c < d; c += kBwdThreads) {
         const size_t at = ((size_t)b * p.H + h) * d + c;
@@ -439,239 +449,366 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     return;
   }
-  const float a_log = p.a_log[h];
-  const HeadGate gate = head_gate(a_log, p.flags & KDA_GATE_SAFE, p.lb);
-  const bool prob = p.flags & KDA_BETA_PROB;
-  float2 bias0, bias1, c0 = both(0.f), c1 = both(0.f);  // c: a D of the token after the cluster's tiles
-  load4(p.dt_bias + (size_t)h * d, d, lane, bias0, bias1);
-  bias0 = mul2(bias0, both(kLog2e));
-  bias1 = mul2(bias1, both(kLog2e));
-  if (p.d_final) load4(p.d_final + ((size_t)b * p.H + h) * d, d, lane, c0, c1);
-
   const size_t row = (size_t)p.H * d;
   const size_t first = (size_t)s0 * row + (size_t)h * d;
-  const TX* x = reinterpret_cast<const TX*>(p.x) + first;
-  const TR* raw = reinterpret_cast<const TR*>(p.raw_gate) + first;
-  const TO* dout = reinterpret_cast<const TO*>(p.dout) + first;
-  const float* beta = p.beta + (size_t)s0 * p.H + h;
-  const float* kept = p.checkpoints + ((size_t)(s0 / kTile + b) * p.H + h) * d;
   const int tiles = (n + kTile - 1) / kTile, steps = (tiles + ranks - 1) / ranks;
-
+  const int pitch = how == kTensor ? d : kRow;
   // step 0 takes the last tiles; rank k the k-th from the end of the step's
   auto tile_of = [&](int step) { return tiles - 1 - (step * ranks + rank); };
-  auto fetch = [&](int step) {
-    const int stage = step % kStages, tile = tile_of(step), t0 = tile * kTile + warp * kBwdRows;
-    if (step < steps && tile >= 0) {
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) sm100::mbar_init(sm100::smem_addr(&sm.full[s]), 1);
+    for (int s = 0; s < 2; ++s) {
+      sm100::mbar_init(sm100::smem_addr(&sm.mapped[s]), kBwdWarps);
+      sm100::mbar_init(sm100::smem_addr(&sm.entered[s]), kCarryWarps);
+      sm100::mbar_init(sm100::smem_addr(&sm.tiles_in[s]), 1);
+      sm100::mbar_init(sm100::smem_addr(&sm.done[s]), kBwdWarps);
+    }
+    sm100::fence_mbar_init();
+  }
+  if (how != kTensor && d < kRow) {  // channels past the head must add nothing to the sums over channels
+    for (size_t i = threadIdx.x; i < offsetof(Smem, map) / 16; i += kBwdThreads)
+      reinterpret_cast<uint4*>(&sm)[i] = make_uint4(0, 0, 0, 0);
+  }
+  cluster.sync();
+  auto wait = [&](uint64_t* bar, int parity) {
+    if (!sm100::mbar_wait_sleep(sm100::smem_addr(bar), parity & 1, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+  };
+
+  if (warp >= kBwdWarps) {
+    // ---------------------------------------------------------------- carrying warps
+    const int c = threadIdx.x - 32 * kBwdWarps;
+    auto fetch = [&](int step) {
+      if (how != kTensor || c != 0 || step >= steps) return;
+      const int stage = step % kStages, tile = tile_of(step), t = s0 + tile * kTile;
+      const uint32_t bar = sm100::smem_addr(&sm.full[stage]);
+      if (tile < 0) return sm100::mbar_arrive(bar);
+      sm100::mbar_arrive_expect_tx(bar, kTile * d * (uint32_t)(sizeof(TX) + sizeof(TR) + sizeof(TO)));
+      sm100::tma_load_3d(sm100::smem_addr(sm.x[stage]), &maps.x, 0, h, t, bar);
+      sm100::tma_load_3d(sm100::smem_addr(sm.raw[stage]), &maps.raw, 0, h, t, bar);
+      sm100::tma_load_3d(sm100::smem_addr(sm.dout[stage]), &maps.dout, 0, h, t, bar);
+    };
+    for (int s = 0; s < kStages - 1; ++s) fetch(s);
+    const float* kept = p.checkpoints + ((size_t)(s0 / kTile + b) * p.H + h) * d + c;
+    auto entering = [&](int step) {
+      const int tile = tile_of(step);
+      return step < steps && tile >= 0 && c < d ? kept[(size_t)tile * row] : 0.f;
+    };
+    const size_t at = ((size_t)b * p.H + h) * d + c;
+    float carry = p.d_final && c < d ? p.d_final[at] : 0.f;  // a D of the token after the cluster's tiles
+    float state = entering(0);
+    for (int step = 0; step < steps; ++step) {
+      const int par = step & 1, buf = kAhead ? par : 0;
+      wait(&sm.mapped[par], step >> 1);
+      float2 of[kBwdWarps];
+      float back[kBwdWarps], pa = 1.f, pb = 0.f;
+#pragma unroll
+      for (int w = 0; w < kBwdWarps; ++w) {
+        of[w] = sm.map[buf][w][c];
+        back[w] = sm.rev[buf][w][c];
+      }
+#pragma unroll
+      for (int w = kBwdWarps - 1; w >= 0; --w) {
+        pb = fmaf(pb, of[w].x, back[w]);
+        pa *= of[w].x;
+      }
+      for (int k = 0; k < ranks; ++k) send_map(&sm.tile_map[par][rank][c], &sm.tiles_in[par], k, pa, pb);
+      if (c == 0)
+        sm100::mbar_arrive_expect_tx(sm100::smem_addr(&sm.tiles_in[par]), ranks * kRow * (uint32_t)sizeof(float2));
+#pragma unroll
+      for (int w = 0; w < kBwdWarps; ++w) {  // the state entering each warp's tokens, over B
+        const float in = state;
+        state = fmaf(state, of[w].x, of[w].y);
+        of[w].y = in;
+      }
+      state = entering(step + 1);
+      wait(&sm.tiles_in[par], step >> 1);
+      float in = carry;
+      float2 m[kMaxCluster];
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) m[k] = k < ranks ? sm.tile_map[par][k][c] : make_float2(1.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        if (k == rank) in = carry;
+        carry = fmaf(carry, m[k].x, m[k].y);
+      }
+#pragma unroll
+      for (int w = kBwdWarps - 1; w >= 0; --w) {
+        sm.map[buf][w][c] = make_float2(of[w].y, in);
+        in = fmaf(in, of[w].x, back[w]);
+      }
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(sm100::smem_addr(&sm.entered[par]));
+      // the next tile goes where the last step's gradients have left
+      if (step > 0 && c == 0) wait(&sm.done[(step - 1) & 1], (step - 1) >> 1);
+      fetch(step + kStages - 1);
+    }
+    if (rank == 0 && c < d) p.d_initial[at] = carry;
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- computing warps
+    const HeadGate gate = head_gate(p.a_log[h], p.flags & KDA_GATE_SAFE, p.lb);
+    const float cut = p.flags & KDA_GATE_SAFE ? gate.lb2 : nanf("");  // gates at or below it pass no gradient
+    const bool prob = p.flags & KDA_BETA_PROB;
+    float2 bias0, bias1;
+    load4(p.dt_bias + (size_t)h * d, d, lane, bias0, bias1);
+    bias0 = mul2(bias0, both(kLog2e));
+    bias1 = mul2(bias1, both(kLog2e));
+    const int row0 = warp * kBwdRows, own = row0 + (lane & (kBwdRows - 1));
+    const float* beta = p.beta + (size_t)s0 * p.H + h;
+    auto load_beta = [&](int step) {
+      const int tile = tile_of(step), t = tile * kTile + own;
+      return step < steps && tile >= 0 && t < n ? beta[(size_t)t * p.H] : 0.f;
+    };
+    auto copy = [&](int step) {  // without tensor copies, the warp's own rows of a step's tile
+      const int tile = tile_of(step), t0 = tile * kTile + row0;
+      const int rows = step < steps && tile >= 0 ? min(max(n - t0, 0), kBwdRows) : 0;
+      const size_t at = first + (size_t)t0 * row;
+      for (int r = 0; r < rows; ++r) {
+        const int to = (row0 + r) * kRow, stage = step % kStages;
+        copy_row(sm.x[stage] + to, reinterpret_cast<const TX*>(p.x) + at + r * row, d, lane, how);
+        copy_row(sm.raw[stage] + to, reinterpret_cast<const TR*>(p.raw_gate) + at + r * row, d, lane, how);
+        copy_row(sm.dout[stage] + to, reinterpret_cast<const TO*>(p.dout) + at + r * row, d, lane, how);
+      }
+      cp_async_commit();
+    };
+    if (how != kTensor)
+      for (int s = 0; s < kStages - 1; ++s) copy(s);
+    float next_bt = beta_fast(load_beta(0), prob), later_beta = load_beta(1);
+    float2 sum_bias0 = both(0.f), sum_bias1 = both(0.f), sum_log = both(0.f);
+    const float2 one = both(1.f), zero = both(0.f);
+
+    struct Kept {
+      float2 g0[kBwdRows], g1[kBwdRows];  // gates (log2) before the clamp
+      float bt;
+    };
+    auto decay = [&](float2 g) {
+      const float2 cg = clamp2(g, gate.lb2);
+      return make_float2(ex2(cg.x), ex2(cg.y));
+    };
+    auto input = [&](float2 x, float bt, float2 g, float2 a) {
+      float2 in = mul2(x, both(bt));
+      if constexpr (kNorm) {
+        const float2 u = one_minus_sq(clamp2(g, gate.lb2), a);
+        in = mul2(in, mul2(u, rsq2(u)));
+      }
+      return in;
+    };
+    auto work_out = [&](int step, Kept& k) {
+      const int stage = step % kStages, par = step & 1, buf = kAhead ? par : 0;
+      k.bt = next_bt;
+      if (how == kTensor) {
+        wait(&sm.full[stage], step / kStages);
+      } else {
+        __syncwarp();
+        if (kAhead && step > 0) copy(step + kStages - 2);
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+      }
+      const TX* xs = sm.x[stage] + row0 * pitch + 4 * lane;
+      const TR* raws = sm.raw[stage] + row0 * pitch + 4 * lane;
+      const TO* douts = sm.dout[stage] + row0 * pitch + 4 * lane;
+      const int tile = tile_of(step), left = tile >= 0 ? n - tile * kTile - row0 : 0;
+      Map4 m{one, one, zero, zero};
+      float2 e0 = zero, e1 = zero, a0[kBwdRows], a1[kBwdRows];
 #pragma unroll
       for (int r = 0; r < kBwdRows; ++r) {
-        if (t0 + r < n) {
-          copy_row(sm.x[stage][warp * kBwdRows + r], x + (t0 + r) * row, d, lane, how);
-          copy_row(sm.raw[stage][warp * kBwdRows + r], raw + (t0 + r) * row, d, lane, how);
-          copy_row(sm.dout[stage][warp * kBwdRows + r], dout + (t0 + r) * row, d, lane, how);
-        }
-      }
-      if (lane < kBwdRows && t0 + lane < n)
-        cp_async<4>(&sm.beta[stage][warp * kBwdRows + lane], beta + (size_t)(t0 + lane) * p.H);
-    }
-    cp_async_commit();
-  };
-  if (d < kRow) {  // channels past the head must add nothing to the sums over channels
-    static_assert(offsetof(Smem, beta) % 16 == 0, "the inputs are cleared in words of 16 bytes");
-    for (size_t i = threadIdx.x; i < offsetof(Smem, beta) / 16; i += kBwdThreads)
-      reinterpret_cast<uint4*>(&sm)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(s);
-
-  float2 sum_bias0 = both(0.f), sum_bias1 = both(0.f), sum_log = both(0.f);
-  const float2 one = both(1.f), zero = both(0.f);
-
-  for (int step = 0; step < steps; ++step) {
-    __syncwarp();  // the stage that is filled next has been read
-    fetch(step + kStages - 1);
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
-    const int stage = step % kStages, par = step & 1;
-    const int tile = tile_of(step), t0 = tile * kTile + warp * kBwdRows;
-    const bool some = tile >= 0;
-    float2 in0 = zero, in1 = zero;  // the state entering the tile
-    if (some) load4(kept + (size_t)tile * row, d, lane, in0, in1);
-
-    // ---- gates, inputs and this warp's maps, forwards and backwards
-    float bt = 0.f;
-    if (lane < kBwdRows) bt = beta_f32(sm.beta[stage][warp * kBwdRows + lane], prob);
-    float2 g0[kBwdRows], g1[kBwdRows], a0[kBwdRows], a1[kBwdRows], b0[kBwdRows], b1[kBwdRows];
-    float2 q0[kBwdRows], q1[kBwdRows];  // s and, with the normalised input, what ds/dg needs
-    Map4 mine{one, one, zero, zero};
-#pragma unroll
-    for (int r = 0; r < kBwdRows; ++r) {
-      const float bt_r = __shfl_sync(0xffffffffu, bt, r);
-      a0[r] = a1[r] = one;
-      b0[r] = b1[r] = zero;
-      if (some && t0 + r < n) {
+        const float bt_r = __shfl_sync(0xffffffffu, k.bt, r);
         float2 z0, z1, x0, x1;
-        unpack4(&sm.raw[stage][warp * kBwdRows + r][4 * lane], z0, z1);
-        unpack4(&sm.x[stage][warp * kBwdRows + r][4 * lane], x0, x1);
+        unpack4(raws + r * pitch, z0, z1);
+        unpack4(xs + r * pitch, x0, x1);
         z0 = pre_log2(z0, bias0);
         z1 = pre_log2(z1, bias1);
-        g0[r] = gate_log2(z0, exp_neg_abs(z0), gate.c);
-        g1[r] = gate_log2(z1, exp_neg_abs(z1), gate.c);
-        const float2 cg0 = clamp2(g0[r], gate.lb2), cg1 = clamp2(g1[r], gate.lb2);
-        a0[r] = make_float2(ex2(cg0.x), ex2(cg0.y));
-        a1[r] = make_float2(ex2(cg1.x), ex2(cg1.y));
-        b0[r] = mul2(x0, both(bt_r));
-        b1[r] = mul2(x1, both(bt_r));
-        if constexpr (kNorm) {
-          const float2 u0 = one_minus_sq(cg0, a0[r]), u1 = one_minus_sq(cg1, a1[r]);
-          q0[r] = mul2(u0, rsq2(u0));
-          q1[r] = mul2(u1, rsq2(u1));
-          b0[r] = mul2(b0[r], q0[r]);
-          b1[r] = mul2(b1[r], q1[r]);
+        k.g0[r] = gate_log2(z0, exp_neg_abs(z0), gate.c);
+        k.g1[r] = gate_log2(z1, exp_neg_abs(z1), gate.c);
+        a0[r] = decay(k.g0[r]);
+        a1[r] = decay(k.g1[r]);
+        float2 b0 = input(x0, bt_r, k.g0[r], a0[r]), b1 = input(x1, bt_r, k.g1[r], a1[r]);
+        if (r >= left) {  // rows past the end are the identity
+          a0[r] = a1[r] = one;
+          b0 = b1 = zero;
         }
-        mine.a0 = mul2(mine.a0, a0[r]);
-        mine.a1 = mul2(mine.a1, a1[r]);
-        mine.b0 = fma2(mine.b0, a0[r], b0[r]);
-        mine.b1 = fma2(mine.b1, a1[r], b1[r]);
+        m.a0 = mul2(m.a0, a0[r]);
+        m.a1 = mul2(m.a1, a1[r]);
+        m.b0 = fma2(m.b0, a0[r], b0);
+        m.b1 = fma2(m.b1, a1[r], b1);
       }
-    }
-    float2 e0 = zero, e1 = zero;  // a_t D_t of the warp's first token, from nothing behind the warp
 #pragma unroll
-    for (int r = kBwdRows - 1; r >= 0; --r) {
-      if (some && t0 + r < n) {
+      for (int r = kBwdRows - 1; r >= 0; --r) {
         float2 o0, o1;
-        unpack4(&sm.dout[stage][warp * kBwdRows + r][4 * lane], o0, o1);
-        e0 = mul2(a0[r], add2(e0, o0));
-        e1 = mul2(a1[r], add2(e1, o1));
+        unpack4(douts + r * pitch, o0, o1);
+        if (r < left) {
+          e0 = mul2(a0[r], add2(e0, o0));
+          e1 = mul2(a1[r], add2(e1, o1));
+        }
       }
-    }
-    write_map(sm.fwd_map[warp], lane, mine);
-    *reinterpret_cast<float4*>(&sm.rev_b[warp][4 * lane]) = make_float4(e0.x, e0.y, e1.x, e1.y);
-    __syncthreads();
-
-    // ---- the state entering this warp's tokens, and what comes back from the warps behind it
-    for (int w = 0; w < warp; ++w) {
-      const Map4 m = read_map(sm.fwd_map[w], lane);
-      in0 = fma2(m.a0, in0, m.b0);
-      in1 = fma2(m.a1, in1, m.b1);
-    }
-    Map4 behind{one, one, zero, zero};
-    auto fold_rev = [&](int w) {
-      const float4 a = *reinterpret_cast<const float4*>(&sm.fwd_map[w].a[4 * lane]);
-      const float4 e = *reinterpret_cast<const float4*>(&sm.rev_b[w][4 * lane]);
-      const float2 wa0 = make_float2(a.x, a.y), wa1 = make_float2(a.z, a.w);
-      behind.a0 = mul2(behind.a0, wa0);
-      behind.a1 = mul2(behind.a1, wa1);
-      behind.b0 = fma2(behind.b0, wa0, make_float2(e.x, e.y));
-      behind.b1 = fma2(behind.b1, wa1, make_float2(e.z, e.w));
+      float4* to = reinterpret_cast<float4*>(&sm.map[buf][warp][4 * lane]);
+      to[0] = make_float4(m.a0.x, m.b0.x, m.a0.y, m.b0.y);
+      to[1] = make_float4(m.a1.x, m.b1.x, m.a1.y, m.b1.y);
+      *reinterpret_cast<float4*>(&sm.rev[buf][warp][4 * lane]) = make_float4(e0.x, e0.y, e1.x, e1.y);
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(sm100::smem_addr(&sm.mapped[par]));
+      next_bt = beta_fast(later_beta, prob);
+      later_beta = load_beta(step + 2);
     };
-    for (int w = kBwdWarps - 1; w > warp; --w) fold_rev(w);
-    if (warp == 0) {
-      const Map4 keep = behind;
-      fold_rev(0);
-      for (int k = 0; k < ranks; ++k) write_map(*cluster.map_shared_rank(&sm.tile_map[par][rank], k), lane, behind);
-      behind = keep;
-    }
-    cluster.sync();
-    float2 back0 = c0, back1 = c1;
-    for (int k = 0; k < ranks; ++k) {
-      if (k == rank) back0 = c0, back1 = c1;
-      const Map4 m = read_map(sm.tile_map[par][k], lane);
-      c0 = fma2(c0, m.a0, m.b0);
-      c1 = fma2(c1, m.a1, m.b1);
-    }
-    if (!some || t0 >= n) continue;
-    back0 = fma2(behind.a0, back0, behind.b0);
-    back1 = fma2(behind.a1, back1, behind.b1);
-
-    // ---- states before each token (over b, which they are made of), then the gradients backwards
-#pragma unroll
-    for (int r = 0; r < kBwdRows; ++r) {
-      const float2 h0 = in0, h1 = in1;
-      in0 = fma2(a0[r], in0, b0[r]);
-      in1 = fma2(a1[r], in1, b1[r]);
-      b0[r] = h0;
-      b1[r] = h1;
-    }
-    float dots[kBwdRows];
-#pragma unroll
-    for (int r = kBwdRows - 1; r >= 0; --r) {
-      dots[r] = 0.f;
-      const float bt_r = __shfl_sync(0xffffffffu, bt, r);
-      if (t0 + r >= n) continue;
-      float2 z0, z1, x0, x1, D0, D1;
-      unpack4(&sm.raw[stage][warp * kBwdRows + r][4 * lane], z0, z1);
-      unpack4(&sm.x[stage][warp * kBwdRows + r][4 * lane], x0, x1);
-      unpack4(&sm.dout[stage][warp * kBwdRows + r][4 * lane], D0, D1);
-      D0 = add2(D0, back0);
-      D1 = add2(D1, back1);
-      back0 = mul2(a0[r], D0);
-      back1 = mul2(a1[r], D1);
-      float2 dg0 = mul2(back0, b0[r]), dg1 = mul2(back1, b1[r]);  // D a h_{t-1}
-      float2 xs0 = mul2(D0, x0), xs1 = mul2(D1, x1);              // D x, times s for dbeta
-      float2 dx0 = mul2(D0, both(bt_r)), dx1 = mul2(D1, both(bt_r));
-      if constexpr (kNorm) {
-        auto slope = [](float2 a, float2 s) {  // ds/dg = -a^2 / s
-          return make_float2(__fdividef(-a.x * a.x, s.x), __fdividef(-a.y * a.y, s.y));
-        };
-        dg0 = fma2(mul2(xs0, both(bt_r)), slope(a0[r], q0[r]), dg0);
-        dg1 = fma2(mul2(xs1, both(bt_r)), slope(a1[r], q1[r]), dg1);
-        xs0 = mul2(xs0, q0[r]);
-        xs1 = mul2(xs1, q1[r]);
-        dx0 = mul2(dx0, q0[r]);
-        dx1 = mul2(dx1, q1[r]);
+    const bool lane_in = 4 * lane < d, wide = vec_grad && lane_in;
+    auto finish = [&](int step, const Kept& k) {
+      const int stage = step % kStages, par = step & 1, buf = kAhead ? par : 0;
+      if (step > 0) {  // the last step's gradients have left shared memory: its tile may be replaced
+        if (lane == 0) {
+          sm100::bulk_wait_read_all();
+          sm100::mbar_arrive(sm100::smem_addr(&sm.done[(step - 1) & 1]));
+        }
+        __syncwarp();
       }
-      // clamped gates pass no gradient; an infinite gate (its decay and dg are 0) counts as finite
-      auto passed = [&](float dg, float g) { return g > gate.lb2 || gate.lb2 == -INFINITY ? dg : 0.f; };
-      dg0 = make_float2(passed(dg0.x, g0[r].x), passed(dg0.y, g0[r].y));
-      dg1 = make_float2(passed(dg1.x, g1[r].x), passed(dg1.y, g1[r].y));
-      const float2 lim = both(-3.0e38f);
-      sum_log = fma2(dg0, make_float2(fmaxf(g0[r].x, lim.x), fmaxf(g0[r].y, lim.y)), sum_log);
-      sum_log = fma2(dg1, make_float2(fmaxf(g1[r].x, lim.x), fmaxf(g1[r].y, lim.y)), sum_log);
-      z0 = pre_log2(z0, bias0);
-      z1 = pre_log2(z1, bias1);
-      auto sigmoid = [](float z) {  // e / (1 + e) or 1 / (1 + e) with e = exp(-|z|), z being in units of log2
-        const float e = ex2(-fabsf(z));
-        return (z >= 0.f ? 1.f : e) * rcp(1.f + e);
-      };
-      const float2 dr0 = mul2(mul2(dg0, both(gate.c)), make_float2(sigmoid(z0.x), sigmoid(z0.y)));
-      const float2 dr1 = mul2(mul2(dg1, both(gate.c)), make_float2(sigmoid(z1.x), sigmoid(z1.y)));
-      sum_bias0 = add2(sum_bias0, dr0);
-      sum_bias1 = add2(sum_bias1, dr1);
-      const int c = 4 * lane;
-      dots[r] = (c < d ? xs0.x : 0.f) + (c + 1 < d ? xs0.y : 0.f) + (c + 2 < d ? xs1.x : 0.f) + (c + 3 < d ? xs1.y : 0.f);
-      const size_t at = first + (size_t)(t0 + r) * row;
-      put4(reinterpret_cast<TX*>(p.dx) + at, d, lane, dx0, dx1, vec_grad);
-      put4(reinterpret_cast<TR*>(p.draw) + at, d, lane, dr0, dr1, vec_grad);
+      wait(&sm.entered[par], step >> 1);
+      const int tile = tile_of(step), left = tile >= 0 ? n - tile * kTile - row0 : 0;
+      const float4* from = reinterpret_cast<const float4*>(&sm.map[buf][warp][4 * lane]);
+      const float4 lo = from[0], hi = from[1];
+      if (left <= 0) return;
+      float2 h0 = make_float2(lo.x, lo.z), h1 = make_float2(hi.x, hi.z);
+      float2 back0 = make_float2(lo.y, lo.w), back1 = make_float2(hi.y, hi.w);
+      TX* xs = sm.x[stage] + row0 * pitch + 4 * lane;
+      TR* raws = sm.raw[stage] + row0 * pitch + 4 * lane;
+      const TO* douts = sm.dout[stage] + row0 * pitch + 4 * lane;
+      const size_t at = first + (size_t)(tile * kTile + row0) * row;
+      // states before each token
+      float2 before[kBwdRows][2];
+#pragma unroll
+      for (int r = 0; r < kBwdRows; ++r) {
+        before[r][0] = h0;
+        before[r][1] = h1;
+        if (r + 1 < kBwdRows) {
+          const float bt_r = __shfl_sync(0xffffffffu, k.bt, r);
+          float2 x0, x1;
+          unpack4(xs + r * pitch, x0, x1);
+          const float2 a0 = decay(k.g0[r]), a1 = decay(k.g1[r]);
+          h0 = fma2(a0, h0, input(x0, bt_r, k.g0[r], a0));
+          h1 = fma2(a1, h1, input(x1, bt_r, k.g1[r], a1));
+        }
+      }
+      float dots[kBwdRows];
+      const bool copied = by_copy && left >= kBwdRows;
+#pragma unroll
+      for (int r = kBwdRows - 1; r >= 0; --r) {
+        dots[r] = 0.f;
+        const float bt_r = __shfl_sync(0xffffffffu, k.bt, r);
+        if (r >= left) continue;
+        float2 z0, z1, x0, x1, D0, D1;
+        unpack4(raws + r * pitch, z0, z1);
+        unpack4(xs + r * pitch, x0, x1);
+        unpack4(douts + r * pitch, D0, D1);
+        const float2 a0 = decay(k.g0[r]), a1 = decay(k.g1[r]);
+        D0 = add2(D0, back0);
+        D1 = add2(D1, back1);
+        back0 = mul2(a0, D0);
+        back1 = mul2(a1, D1);
+        float2 dg0 = mul2(back0, before[r][0]), dg1 = mul2(back1, before[r][1]);  // D a h_{t-1}
+        float2 xs0 = mul2(D0, x0), xs1 = mul2(D1, x1);                  // D x, times s for dbeta
+        float2 dx0 = mul2(D0, both(bt_r)), dx1 = mul2(D1, both(bt_r));
+        if constexpr (kNorm) {
+          const float2 u0 = one_minus_sq(clamp2(k.g0[r], gate.lb2), a0), u1 = one_minus_sq(clamp2(k.g1[r], gate.lb2), a1);
+          const float2 i0 = rsq2(u0), i1 = rsq2(u1), s0v = mul2(u0, i0), s1v = mul2(u1, i1);
+          // ds/dg = -a^2 / s
+          dg0 = fma2(mul2(xs0, both(-bt_r)), mul2(mul2(a0, a0), i0), dg0);
+          dg1 = fma2(mul2(xs1, both(-bt_r)), mul2(mul2(a1, a1), i1), dg1);
+          xs0 = mul2(xs0, s0v);
+          xs1 = mul2(xs1, s1v);
+          dx0 = mul2(dx0, s0v);
+          dx1 = mul2(dx1, s1v);
+        }
+        auto passed = [&](float dg, float g) { return !(g <= cut) ? dg : 0.f; };
+        dg0 = make_float2(passed(dg0.x, k.g0[r].x), passed(dg0.y, k.g0[r].y));
+        dg1 = make_float2(passed(dg1.x, k.g1[r].x), passed(dg1.y, k.g1[r].y));
+        // an infinite gate (its decay and dg are 0) counts as a finite one
+        auto finite = [](float2 g) { return make_float2(fmaxf(g.x, -3.0e38f), fmaxf(g.y, -3.0e38f)); };
+        sum_log = fma2(dg0, finite(k.g0[r]), sum_log);
+        sum_log = fma2(dg1, finite(k.g1[r]), sum_log);
+        z0 = pre_log2(z0, bias0);
+        z1 = pre_log2(z1, bias1);
+        auto sigmoid = [](float z) {  // e / (1 + e) or 1 / (1 + e) with e = exp(-|z|), z being in units of log2
+          const float e = ex2(-fabsf(z));
+          return (z >= 0.f ? 1.f : e) * rcp(1.f + e);
+        };
+        const float2 dr0 = mul2(mul2(dg0, both(gate.c)), make_float2(sigmoid(z0.x), sigmoid(z0.y)));
+        const float2 dr1 = mul2(mul2(dg1, both(gate.c)), make_float2(sigmoid(z1.x), sigmoid(z1.y)));
+        sum_bias0 = add2(sum_bias0, dr0);
+        sum_bias1 = add2(sum_bias1, dr1);
+        dots[r] = lane_in ? (xs0.x + xs0.y) + (xs1.x + xs1.y) : 0.f;
+        if (copied) {
+          if (lane_in) {
+            store4(xs + r * pitch, dx0, dx1);
+            store4(raws + r * pitch, dr0, dr1);
+          }
+        } else if (wide) {
+          store4(reinterpret_cast<TX*>(p.dx) + at + r * row + 4 * lane, dx0, dx1);
+          store4(reinterpret_cast<TR*>(p.draw) + at + r * row + 4 * lane, dr0, dr1);
+        } else if (!vec_grad) {
+          put4(reinterpret_cast<TX*>(p.dx) + at + r * row, d, lane, dx0, dx1, false);
+          put4(reinterpret_cast<TR*>(p.draw) + at + r * row, d, lane, dr0, dr1, false);
+        }
+      }
+      if (copied) {
+        sm100::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const int t = s0 + tile * kTile + row0;
+          sm100::tma_store_3d(&maps.dx, sm100::smem_addr(sm.x[stage] + row0 * pitch), 0, h, t);
+          sm100::tma_store_3d(&maps.draw, sm100::smem_addr(sm.raw[stage] + row0 * pitch), 0, h, t);
+          sm100::bulk_commit();
+        }
+      }
+      // ---- dbeta of the warp's four tokens: halves of the lanes take two each, quarters one
+      static_assert(kBwdRows == 4, "the reduction is written for four tokens");
+      const bool upper = lane & 16, odd = lane & 8;
+      float u = (upper ? dots[2] : dots[0]) + __shfl_xor_sync(0xffffffffu, upper ? dots[0] : dots[2], 16);
+      float v = (upper ? dots[3] : dots[1]) + __shfl_xor_sync(0xffffffffu, upper ? dots[1] : dots[3], 16);
+      float w = (odd ? v : u) + __shfl_xor_sync(0xffffffffu, odd ? u : v, 8);
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      const int r = lane >> 3;
+      const float bt_r = __shfl_sync(0xffffffffu, k.bt, r);
+      if ((lane & 7) == 0 && r < left)
+        p.dbeta[(size_t)(s0 + tile * kTile + row0 + r) * p.H + h] = prob ? w : w * bt_r * (1.f - bt_r);
+    };
+    if constexpr (kAhead) {
+      Kept even, odd;
+      work_out(0, even);
+      for (int step = 0; step < steps; step += 2) {
+        if (step + 1 < steps) work_out(step + 1, odd);
+        finish(step, even);
+        if (step + 1 >= steps) break;
+        if (step + 2 < steps) work_out(step + 2, even);
+        finish(step + 1, odd);
+      }
+    } else {
+      Kept k;
+      for (int step = 0; step < steps; ++step) {
+        work_out(step, k);
+        finish(step, k);
+        if (how != kTensor) {
+          __syncwarp();
+          copy(step + kStages - 1);
+        }
+      }
     }
-    // ---- dbeta of the warp's tokens
+    sm100::bulk_wait_all();
+    // ---- the warp's share of the parameters' gradients
+    float* red = &sm.rev[0][0][0];  // [warps][kRow]
+    named_barrier_sync<1, 32 * kBwdWarps>();  // the carrying warps have read the last step's (it has been entered)
+    *reinterpret_cast<float4*>(red + warp * kRow + 4 * lane) = make_float4(sum_bias0.x, sum_bias0.y, sum_bias1.x, sum_bias1.y);
+    float lg = lane_in ? sum_log.x + sum_log.y : 0.f;
 #pragma unroll
-    for (int r = 0; r < kBwdRows; ++r) {
+    for (int o = 16; o >= 1; o >>= 1) lg += __shfl_xor_sync(0xffffffffu, lg, o);
+    float* red_log = reinterpret_cast<float*>(&sm.map[0][0][0]);
+    if (lane == 0) red_log[warp] = lg;
+    named_barrier_sync<1, 32 * kBwdWarps>();
+    for (int i = threadIdx.x; i <= d; i += 32 * kBwdWarps) {
+      float s = 0.f;
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) dots[r] += __shfl_xor_sync(0xffffffffu, dots[r], o);
+      for (int w = 0; w < kBwdWarps; ++w) s += i < d ? red[w * kRow + i] : red_log[w];
+      part[i] = i < d ? s : s * kLn2;  // the last one: dg g, g having been kept times log2 e
     }
-#pragma unroll
-    for (int r = 0; r < kBwdRows; ++r)
-      if (lane == r && t0 + r < n)
-        p.dbeta[(size_t)(s0 + t0 + r) * p.H + h] = prob ? dots[r] : dots[r] * bt * (1.f - bt);
-  }
-  if (rank == 0 && warp == 0) put4(p.d_initial + ((size_t)b * p.H + h) * d, d, lane, c0, c1, false);
-
-  // ---- the CTA's share of the parameters' gradients, summed over the warps in order
-  __syncthreads();
-  float* red = &sm.rev_b[0][0];  // [warps][kRow]
-  *reinterpret_cast<float4*>(red + warp * kRow + 4 * lane) = make_float4(sum_bias0.x, sum_bias0.y, sum_bias1.x, sum_bias1.y);
-  float lg = sum_log.x + sum_log.y;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) lg += __shfl_xor_sync(0xffffffffu, lg, o);
-  float* red_log = &sm.fwd_map[0].a[0];
-  if (lane == 0) red_log[warp] = lg;
-  __syncthreads();
-  for (int i = threadIdx.x; i <= d; i += kBwdThreads) {
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kBwdWarps; ++w) s += i < d ? red[w * kRow + i] : red_log[w];
-    part_bias[i] = i < d ? s : s * kLn2;  // the last one: dg g, g having been kept times log2 e
   }
 }
 
@@ -837,15 +974,24 @@ cudaError_t fwd(const GlrArgs& a, cudaStream_t stream) {
 
 template <typename TX, typename TR, typename TO>
 cudaError_t bwd(const GlrBwdArgs& a, cudaStream_t stream) {
-  const Access how =
-      worse(worse(access_of<TX>(a.x, a.d), access_of<TR>(a.raw_gate, a.d)), access_of<TO>(a.dout, a.d));
+  Access how = worse(worse(access_of<TX>(a.x, a.d), access_of<TR>(a.raw_gate, a.d)), access_of<TO>(a.dout, a.d));
+  BwdMaps maps{};
+  const int64_t T = a.total_tokens;
+  if (how == kTensor && (T == 0 || !encode<TX>(&maps.x, a.x, T, a.H, a.d) || !encode<TR>(&maps.raw, a.raw_gate, T, a.H, a.d) ||
+                         !encode<TO>(&maps.dout, a.dout, T, a.H, a.d)))
+    how = kVec4;
+  // a warp's rows leave by tensor copies where they also start on 128 bytes of shared memory
+  const bool by_copy = how == kTensor && access_of<TX>(a.dx, a.d) == kTensor && access_of<TR>(a.draw, a.d) == kTensor &&
+                       kBwdRows * a.d * sizeof(TX) % 128 == 0 && kBwdRows * a.d * sizeof(TR) % 128 == 0 &&
+                       encode<TX>(&maps.dx, a.dx, T, a.H, a.d, kBwdRows) && encode<TR>(&maps.draw, a.draw, T, a.H, a.d, kBwdRows);
   const bool vec_grad = a.d % 4 == 0 && aligned(a.dx, 4 * sizeof(TX)) && aligned(a.draw, 4 * sizeof(TR));
   const int ranks = cluster_size(a.batch, a.total_tokens, a.H, BwdSmem<TX, TR, TO>::kMaxRanks);
   const int64_t grid = (int64_t)a.batch * a.H * ranks;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const size_t smem = sizeof(BwdSmem<TX, TR, TO>);
+  static_assert(sizeof(BwdSmem<TX, TR, TO>) <= 227 * 1024 && sizeof(FwdSmem<TX, TR, TO>) <= 227 * 1024, "");
   const auto kernel = a.flags & KDA_INPUT_NORM ? glr_bwd_kernel<TX, TR, TO, true> : glr_bwd_kernel<TX, TR, TO, false>;
-  cudaError_t e = launch_cluster(kernel, (unsigned)grid, kBwdThreads, smem, ranks, stream, a, how, vec_grad);
+  cudaError_t e = launch_cluster(kernel, (unsigned)grid, kBwdThreads, smem, ranks, stream, a, maps, how, by_copy, vec_grad);
   if (e != cudaSuccess) return e;
   const int64_t sums = (int64_t)a.H * (a.d + 1);
   glr_bwd_sum_kernel<<<(unsigned)((sums * 32 + 255) / 256), 256, 0, stream>>>(a.partial, a.batch * ranks, a.H, a.d,
