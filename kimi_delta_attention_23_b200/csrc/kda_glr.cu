@@ -42,6 +42,7 @@ constexpr int kMaxCluster = 8;
 // How rows of d channels come to shared memory: by tensor copies where rows start on 16 bytes; else
 // four channels per lane at once, in words of 4 bytes, or element by element through registers.
 enum Access { kTensor = 0, kVec4 = 1, kWord = 2, kElem = 3 };
+constexpr float kLeast = -3.0e38f;  // an infinite gate counts as this one: its decay is 0 all the same
 constexpr uint64_t kWaitNs = 1000000000ull;  // limit of a wait for a copy or for another warp
 
 struct Maps {
@@ -185,7 +186,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
   }
   cluster.sync();
   auto wait = [&](uint64_t* bar, int parity) {
-    if (!sm100::mbar_wait_sleep(sm100::smem_addr(bar), parity & 1, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    const uint32_t at = sm100::smem_addr(bar);
+    if (sm100::mbar_try_wait(at, parity & 1)) return;  // nearly always: a sleeping wait takes longer to say so
+    if (!sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
   };
 
   const int pitch = how == kTensor ? d : kRow;  // elements of a tile's row
@@ -345,33 +348,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
   TO* staged = sm.out + row0 * kRow;
   auto finish = [&](int step, const Kept& k) {
     const int par = step & 1, tile = step * ranks + rank, left = n - tile * kTile - row0;
+    const bool copied = out_map && left >= kFwdRows;
+    sm100::bulk_wait_read_all();  // (the issuing lane's) the last rows have left
     wait(&sm.entered[par], step >> 1);
     const float4* from = reinterpret_cast<const float4*>(&sm.map[par][warp][4 * lane]);
     const float4 lo = from[0], hi = from[1];
     float2 in0 = make_float2(lo.x, lo.z), in1 = make_float2(hi.x, hi.z);
-    const bool copied = out_map && left >= kFwdRows;
-    if (copied) {
-      sm100::bulk_wait_read_all();  // (the issuing lane's) the rows have left
-      __syncwarp();
-    }
-    TO* to = out + (size_t)tile * kTile * row;
+    float2 h0[kFwdRows], h1[kFwdRows];
 #pragma unroll
-    for (int r = 0; r < kFwdRows; ++r, to += row) {
-      in0 = fma2(k.a0[r], in0, k.b0[r]);
-      in1 = fma2(k.a1[r], in1, k.b1[r]);
-      if (copied) {
-        if (4 * lane < d) store4(staged + r * d + 4 * lane, in0, in1);
-      } else if (r < left) {
-        put4(to, d, lane, in0, in1, vec_out);
-      }
+    for (int r = 0; r < kFwdRows; ++r) {
+      in0 = h0[r] = fma2(k.a0[r], in0, k.b0[r]);
+      in1 = h1[r] = fma2(k.a1[r], in1, k.b1[r]);
     }
     if (copied) {
+      __syncwarp();
+      if (4 * lane < d) {
+#pragma unroll
+        for (int r = 0; r < kFwdRows; ++r) store4(staged + r * d + 4 * lane, h0[r], h1[r]);
+      }
       sm100::fence_async_smem();
       __syncwarp();
       if (lane == 0) {
         sm100::tma_store_3d(&maps.out, sm100::smem_addr(staged), 0, h, s0 + tile * kTile + row0);
         sm100::bulk_commit();
       }
+    } else {
+      TO* to = out + (size_t)tile * kTile * row;
+#pragma unroll
+      for (int r = 0; r < kFwdRows; ++r)
+        if (r < left) put4(to + r * row, d, lane, h0[r], h1[r], vec_out);
     }
   };
   Kept even, odd;
@@ -420,7 +425,7 @@ struct BwdSmem {
   uint64_t full[kStages], mapped[2], entered[2], tiles_in[2], done[2];
 };
 
-template <typename TX, typename TR, typename TO, bool kNorm>
+template <typename TX, typename TR, typename TO, bool kNorm, bool kSafe>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     glr_bwd_kernel(const GlrBwdArgs p, const __grid_constant__ BwdMaps maps, const Access how, const bool by_copy,
                    const bool vec_grad) {
@@ -472,7 +477,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
   cluster.sync();
   auto wait = [&](uint64_t* bar, int parity) {
-    if (!sm100::mbar_wait_sleep(sm100::smem_addr(bar), parity & 1, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    const uint32_t at = sm100::smem_addr(bar);
+    if (sm100::mbar_try_wait(at, parity & 1)) return;  // nearly always: a sleeping wait takes longer to say so
+    if (!sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
   };
 
   if (warp >= kBwdWarps) {
@@ -547,8 +554,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- computing warps
-    const HeadGate gate = head_gate(p.a_log[h], p.flags & KDA_GATE_SAFE, p.lb);
-    const float cut = p.flags & KDA_GATE_SAFE ? gate.lb2 : nanf("");  // gates at or below it pass no gradient
+    const HeadGate gate = head_gate(p.a_log[h], kSafe, p.lb);
     const bool prob = p.flags & KDA_BETA_PROB;
     float2 bias0, bias1;
     load4(p.dt_bias + (size_t)h * d, d, lane, bias0, bias1);
@@ -579,17 +585,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float2 one = both(1.f), zero = both(0.f);
 
     struct Kept {
-      float2 g0[kBwdRows], g1[kBwdRows];  // gates (log2) before the clamp
+      float2 g0[kBwdRows], g1[kBwdRows];  // gates (log2), clamped, and finite
       float bt;
     };
-    auto decay = [&](float2 g) {
-      const float2 cg = clamp2(g, gate.lb2);
-      return make_float2(ex2(cg.x), ex2(cg.y));
-    };
+    auto decay = [&](float2 g) { return make_float2(ex2(g.x), ex2(g.y)); };
     auto input = [&](float2 x, float bt, float2 g, float2 a) {
       float2 in = mul2(x, both(bt));
       if constexpr (kNorm) {
-        const float2 u = one_minus_sq(clamp2(g, gate.lb2), a);
+        const float2 u = one_minus_sq(g, a);
         in = mul2(in, mul2(u, rsq2(u)));
       }
       return in;
@@ -619,8 +622,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         unpack4(xs + r * pitch, x0, x1);
         z0 = pre_log2(z0, bias0);
         z1 = pre_log2(z1, bias1);
-        k.g0[r] = gate_log2(z0, exp_neg_abs(z0), gate.c);
-        k.g1[r] = gate_log2(z1, exp_neg_abs(z1), gate.c);
+        k.g0[r] = clamp2(gate_log2(z0, exp_neg_abs(z0), gate.c), fmaxf(gate.lb2, kLeast));
+        k.g1[r] = clamp2(gate_log2(z1, exp_neg_abs(z1), gate.c), fmaxf(gate.lb2, kLeast));
         a0[r] = decay(k.g0[r]);
         a1[r] = decay(k.g1[r]);
         float2 b0 = input(x0, bt_r, k.g0[r], a0[r]), b1 = input(x1, bt_r, k.g1[r], a1[r]);
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         float2 xs0 = mul2(D0, x0), xs1 = mul2(D1, x1);                  // D x, times s for dbeta
         float2 dx0 = mul2(D0, both(bt_r)), dx1 = mul2(D1, both(bt_r));
         if constexpr (kNorm) {
-          const float2 u0 = one_minus_sq(clamp2(k.g0[r], gate.lb2), a0), u1 = one_minus_sq(clamp2(k.g1[r], gate.lb2), a1);
+          const float2 u0 = one_minus_sq(k.g0[r], a0), u1 = one_minus_sq(k.g1[r], a1);
           const float2 i0 = rsq2(u0), i1 = rsq2(u1), s0v = mul2(u0, i0), s1v = mul2(u1, i1);
           // ds/dg = -a^2 / s
           dg0 = fma2(mul2(xs0, both(-bt_r)), mul2(mul2(a0, a0), i0), dg0);
@@ -717,19 +720,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           dx0 = mul2(dx0, s0v);
           dx1 = mul2(dx1, s1v);
         }
-        auto passed = [&](float dg, float g) { return !(g <= cut) ? dg : 0.f; };
-        dg0 = make_float2(passed(dg0.x, k.g0[r].x), passed(dg0.y, k.g0[r].y));
-        dg1 = make_float2(passed(dg1.x, k.g1[r].x), passed(dg1.y, k.g1[r].y));
-        // an infinite gate (its decay and dg are 0) counts as a finite one
-        auto finite = [](float2 g) { return make_float2(fmaxf(g.x, -3.0e38f), fmaxf(g.y, -3.0e38f)); };
-        sum_log = fma2(dg0, finite(k.g0[r]), sum_log);
-        sum_log = fma2(dg1, finite(k.g1[r]), sum_log);
+        if constexpr (kSafe) {  // a clamped gate passes no gradient
+          dg0 = make_float2(k.g0[r].x > gate.lb2 ? dg0.x : 0.f, k.g0[r].y > gate.lb2 ? dg0.y : 0.f);
+          dg1 = make_float2(k.g1[r].x > gate.lb2 ? dg1.x : 0.f, k.g1[r].y > gate.lb2 ? dg1.y : 0.f);
+        }
+        sum_log = fma2(dg0, k.g0[r], sum_log);
+        sum_log = fma2(dg1, k.g1[r], sum_log);
         z0 = pre_log2(z0, bias0);
         z1 = pre_log2(z1, bias1);
-        auto sigmoid = [](float z) {  // e / (1 + e) or 1 / (1 + e) with e = exp(-|z|), z being in units of log2
-          const float e = ex2(-fabsf(z));
-          return (z >= 0.f ? 1.f : e) * rcp(1.f + e);
-        };
+        auto sigmoid = [](float z2) { return rcp(1.f + ex2(-z2)); };  // z2 in units of log2
         const float2 dr0 = mul2(mul2(dg0, both(gate.c)), make_float2(sigmoid(z0.x), sigmoid(z0.y)));
         const float2 dr1 = mul2(mul2(dg1, both(gate.c)), make_float2(sigmoid(z1.x), sigmoid(z1.y)));
         sum_bias0 = add2(sum_bias0, dr0);
@@ -890,15 +889,24 @@ __global__ void __launch_bounds__(kDecThreads) glr_decode_kernel(const GlrArgs p
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// CTAs per (sequence, head): the smallest power of two that gives every SM two of them, as long as
-// the average sequence has a tile for each.
+// CTAs per (sequence, head).  One fits an SM at a time, so c of them make ceil(chains c / SMs) rounds of
+// 1 / c of a chain; sequences of unequal lengths leave about one more round half empty, and each CTA of a
+// cluster adds some 4 % to a step.  8 packed sequences of 32 heads (32768 tokens, forward / backward): 1 CTA
+// 272 / 774 us, 2: 243 / 685, 4: 246 / 666, 8: 306 / 666; one of 131072 tokens: 4 989 us, 8 1437 us.
 int cluster_size(int32_t batch, int64_t T, int32_t H, int most) {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t tiles = (T / batch + kTile - 1) / kTile;
-  int c = 1;
-  while (c < most && (int64_t)batch * H * c * 8 < 6 * sms && 2 * c <= tiles) c *= 2;
-  return c;
+  const int64_t tiles = (T / batch + kTile - 1) / kTile, chains = (int64_t)batch * H;
+  int best = 1;
+  double least = 0;
+  for (int c = 1; c <= most && (c == 1 || c <= tiles); c *= 2) {
+    const double cost = (double)((chains * c + sms - 1) / sms + (batch > 1)) / c * (1 + 0.04 * c);
+    if (c == 1 || cost < least) {
+      best = c;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 template <typename Kernel, typename... Args>
@@ -990,7 +998,9 @@ cudaError_t bwd(const GlrBwdArgs& a, cudaStream_t stream) {
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const size_t smem = sizeof(BwdSmem<TX, TR, TO>);
   static_assert(sizeof(BwdSmem<TX, TR, TO>) <= 227 * 1024 && sizeof(FwdSmem<TX, TR, TO>) <= 227 * 1024, "");
-  const auto kernel = a.flags & KDA_INPUT_NORM ? glr_bwd_kernel<TX, TR, TO, true> : glr_bwd_kernel<TX, TR, TO, false>;
+  const bool norm = a.flags & KDA_INPUT_NORM, safe = a.flags & KDA_GATE_SAFE;
+  const auto kernel = norm ? (safe ? glr_bwd_kernel<TX, TR, TO, true, true> : glr_bwd_kernel<TX, TR, TO, true, false>)
+                           : (safe ? glr_bwd_kernel<TX, TR, TO, false, true> : glr_bwd_kernel<TX, TR, TO, false, false>);
   cudaError_t e = launch_cluster(kernel, (unsigned)grid, kBwdThreads, smem, ranks, stream, a, maps, how, by_copy, vec_grad);
   if (e != cudaSuccess) return e;
   const int64_t sums = (int64_t)a.H * (a.d + 1);

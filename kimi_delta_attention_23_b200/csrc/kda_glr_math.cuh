@@ -100,8 +100,14 @@ __device__ __forceinline__ float2 exp_neg_abs(float2 z2) { return make_float2(ex
 __device__ __forceinline__ float2 gate_log2(float2 z2, float2 e, float c) {
   return mul2(both(c), fma2(e, log2_1p_ratio(e), make_float2(fmaxf(z2.x, 0.f), fmaxf(z2.y, 0.f))));
 }
+// (a gate that is not a number stays one)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float2 clamp2(float2 g2, float lb2) {
-  return make_float2(fmaxf(g2.x, lb2), fmaxf(g2.y, lb2));
+  return make_float2(max_nan(g2.x, lb2), max_nan(g2.y, lb2));
 }
 
 // 1 - a^2 for a = 2^g2, at least the smallest normal number: by the polynomial for exp(2 g) - 1 where
