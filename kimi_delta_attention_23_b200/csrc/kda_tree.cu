@@ -32,7 +32,7 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;     // of the commit
 constexpr int kPitch = 132;    // floats of a node's row in shared memory
 constexpr uint64_t kWaitNs = 1000000000ull;  // limit of the wait for a copy
 constexpr int kPitchH = 144;   // bf16 of a row of the split factors (32 bytes past 256: no conflicts)
@@ -72,11 +72,19 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(ry), "f"(rx));
 }
 
+// Up to 16 nodes, four CTAs of four warps share an SM, and each reads the state straight from L2: the
+// phases of so small a tree are all latency, and other CTAs are what fills it.  Beyond, the products
+// carry the time: eight warps, with the state staged in shared memory.
+template <int kNodes>
+constexpr int kTreeThreads = kNodes <= 16 ? 128 : 256;
+template <int kNodes>
+constexpr bool kStaged = kNodes > 16;
+
 template <int kNodes>
 struct TreeSmem {
-  // 64 KB: the state (1), then (K o e^G) S and (Q o e^G) S (2), the former becoming the deltas (3)
+  // the state if it is staged (1), then (K o e^G) S and (Q o e^G) S (2), the former becoming the deltas (3)
   union {
-    alignas(128) float state[128 * 128];
+    alignas(128) float state[kStaged<kNodes> ? 128 * 128 : 4];
     struct {
       float u[kNodes < 16 ? 16 : kNodes][128], qs[kNodes < 16 ? 16 : kNodes][128];
     };
@@ -127,7 +135,10 @@ __device__ __forceinline__ void split_scores(const float* row0, const float* row
 }
 
 template <int kNodes, bool kVFirst, bool kFull, typename T>
-__global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(const TreeArgs p, const bool wide_out) {
+__global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNodes <= 32 ? 2 : 1)
+    tree_kernel(const TreeArgs p, const bool wide_out) {
+  constexpr int kThreads = kTreeThreads<kNodes>, kWarps = kThreads / 32;
+  constexpr int kCols = 8 / kWarps;  // groups of 16 value columns per warp: warp, warp + kWarps, ..
   extern __shared__ __align__(128) unsigned char smem_raw[];
   TreeSmem<kNodes>& sm = *reinterpret_cast<TreeSmem<kNodes>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -145,7 +156,10 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
   }
   if (n == 0) return;
   const float* state = p.pool + ((size_t)slot * p.Hv + h) * (size_t)dk * dv;
-  if constexpr (kFull) {  // the state comes while the scores are worked out
+  if constexpr (kFull && !kStaged<kNodes>) {  // the state comes while the scores are worked out
+    if (tid == 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(state), "r"(128 * 128 * 4) : "memory");
+  } else if constexpr (kFull) {
     if (tid == 0) {
       const uint32_t bar = sm100::smem_addr(&sm.full);
       sm100::mbar_init(bar, 1);
@@ -161,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
   constexpr int kGroup = kThreads / kNodes;  // lanes per node
   constexpr int kQuads = 32 / kGroup;        // float4's of channels per lane
   static_assert(kGroup <= 32 && kQuads >= 1, "");
-  constexpr int kAtOnce = kNodes >= 32 ? 4 : kNodes / 8;  // rows of a warp with their loads in flight together
+  constexpr int kAtOnce = kNodes >= 32 ? 4 : kNodes / kWarps;  // rows of a warp with their loads in flight together
   const int node = tid / kGroup, g = tid % kGroup;
   const int mine = min(tid, n - 1);
   const int32_t parent = p.parents[m0 + mine];
@@ -170,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
   auto load_rows = [&](int m1) {
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
-      const int m = min(m1 + 8 * j, n - 1);
+      const int m = min(m1 + kWarps * j, n - 1);
       kv[j] = load_quad<kFull>(ks + m * k_row, c4, dk);
       raw[j] = load_quad<kFull>(raws + m * raw_row, c4, dk);
     }
@@ -194,11 +208,11 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
     const float2 bias0 = glr::mul2(make_float2(bias.x, bias.y), glr::both(glr::kLog2e));
     const float2 bias1 = glr::mul2(make_float2(bias.z, bias.w), glr::both(glr::kLog2e));
 #pragma unroll 1
-    for (int m1 = warp; m1 < n; m1 += 8 * kAtOnce) {
+    for (int m1 = warp; m1 < n; m1 += kWarps * kAtOnce) {
       if (m1 != warp) load_rows(m1);
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        const int m = m1 + 8 * j;
+        const int m = m1 + kWarps * j;
         const float2 z0 = glr::pre_log2(make_float2(raw[j].x, raw[j].y), bias0);
         const float2 z1 = glr::pre_log2(make_float2(raw[j].z, raw[j].w), bias1);
         const float2 g0 = glr::clamp2(glr::gate_log2(z0, glr::exp_neg_abs(z0), gate.c), gate.lb2);
@@ -211,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
     }
   }
   if (!__syncthreads_and(parent >= -1 && parent < mine)) {
-    if constexpr (kFull) {  // the copy in flight writes to this CTA's memory
+    if constexpr (kFull && kStaged<kNodes>) {  // the copy in flight writes to this CTA's memory
       if (!sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
     }
     if (tid == 0) report(p.status, KDA_ERR_DEVICE_CHECK);
@@ -277,11 +291,13 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
   // 16 warp + 2 (lane / 4) + {0, 1}) over all key channels.  Within each 16 channels a lane's four
   // are 4 (lane % 4) .. + 3 in both operands (the order of the summed index is free), so that its
   // share of V_FIRST states and of the factors is one wide access.
-  if constexpr (kFull) {
+  if constexpr (kFull && kStaged<kNodes>) {
     if (!sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
   }
-  {
-    const int q = lane & 3, gr = lane >> 2, col = 16 * warp + 2 * gr;  // a lane's first column of S
+  const float* from = kFull && kStaged<kNodes> ? sm.state : state;
+#pragma unroll 1
+  for (int group = warp; group < 8; group += kWarps) {
+    const int q = lane & 3, gr = lane >> 2, col = 16 * group + 2 * gr;  // a lane's first column of S
     uint32_t bh[8][2][2], bl[8][2][2];  // [k-step][n-tile][register]
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
@@ -290,13 +306,13 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
       if constexpr (kFull && kVFirst) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float4 v = *reinterpret_cast<const float4*>(sm.state + (col + t) * 128 + c);
+          const float4 v = *reinterpret_cast<const float4*>(from + (col + t) * 128 + c);
           s[t][0] = v.x, s[t][1] = v.y, s[t][2] = v.z, s[t][3] = v.w;
         }
       } else if constexpr (kFull) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 v = *reinterpret_cast<const float2*>(sm.state + (c + e) * 128 + col);
+          const float2 v = *reinterpret_cast<const float2*>(from + (c + e) * 128 + col);
           s[0][e] = v.x, s[1][e] = v.y;
         }
       } else {
@@ -312,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
         split2(s[t][2], s[t][3], bh[ks][t][1], bl[ks][t][1]);
       }
     }
-    __syncthreads();  // the factors are there, and the state has been read: u and qs take its place
+    if (group == warp) __syncthreads();  // the factors are there, and a staged state has been read: u and qs take its place
     const int tiles = (n + 7) >> 3;
     for (int t = 0; t < tiles; ++t) {
       float big[2][4] = {}, small[2][4] = {};
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
         }
       }
       // accumulator n = 2 (lane % 4) + {0, 1} of tile nt is column 16 warp + 2 n + nt
-      const int c0 = 16 * warp + 4 * q, i = 8 * t + gr;
+      const int c0 = 16 * group + 4 * q, i = 8 * t + gr;
       *reinterpret_cast<float4*>(&sm.u[i][c0]) =
           make_float4(big[0][0] + small[0][0], big[1][0] + small[1][0], big[0][1] + small[0][1], big[1][1] + small[1][1]);
       *reinterpret_cast<float4*>(&sm.qs[i][c0]) =
@@ -345,20 +361,30 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
   // as above), the rest a substitution with a thread per value column.  The products run over all
   // nodes, weights being zero where one is no ancestor; a delta that is not finite must not reach
   // other branches through such a zero, so from the first one on, ancestors are walked instead.
-  const int q = lane & 3, gr = lane >> 2, c0 = 16 * warp + 4 * q;  // a lane's columns of the products
+  const int q = lane & 3, gr = lane >> 2;
+  auto c0 = [&](int g) { return 16 * (warp + kWarps * g) + 4 * q; };  // a lane's columns of the products
   const int blocks = (n + 15) >> 4, col = tid & 127;
   const size_t row = (size_t)p.Hv * dv;
   const T* vs = reinterpret_cast<const T*>(p.v) + ((size_t)m0 * p.Hv + h) * dv;
   float* deltas = p.deltas + ((size_t)m0 * p.Hv + h) * dv;
   bool walk = false;
   constexpr int kBlocks = (kNodes + 15) / 16;
-  uint32_t uh[kBlocks][2][2], ul[kBlocks][2][2];  // solved blocks as fragments: [block][n-tile][register]
-  float4 v0 = load_quad<kFull>(vs + min(gr, n - 1) * row, c0, dv), v8 = load_quad<kFull>(vs + min(gr + 8, n - 1) * row, c0, dv);
+  uint32_t uh[kCols][kBlocks][2][2], ul[kCols][kBlocks][2][2];  // solved blocks as fragments: [.][block][n-tile][register]
+  float4 v0[kCols], v8[kCols];
+  auto load_values = [&](int i0) {
+#pragma unroll
+    for (int g = 0; g < kCols; ++g) {
+      v0[g] = load_quad<kFull>(vs + min(i0 + gr, n - 1) * row, c0(g), dv);
+      v8[g] = load_quad<kFull>(vs + min(i0 + gr + 8, n - 1) * row, c0(g), dv);
+    }
+  };
+  load_values(0);
 #pragma unroll
   for (int blk = 0; blk < kBlocks; ++blk) {
     if (blk >= blocks) break;
     const int i0 = 16 * blk;
-    {
+#pragma unroll
+    for (int g = 0; g < kCols; ++g) {
       float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
       for (int kb = 0; kb < blk; ++kb) {
@@ -366,23 +392,20 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
         split_scores(&sm.a[i0 + gr][16 * kb + 4 * q], &sm.a[i0 + gr + 8][16 * kb + 4 * q], ah, al);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-          mma_bf16(big[nt], ah, uh[kb][nt][0], uh[kb][nt][1]);
-          mma_bf16(small[nt], al, uh[kb][nt][0], uh[kb][nt][1]);
-          mma_bf16(small[nt], ah, ul[kb][nt][0], ul[kb][nt][1]);
+          mma_bf16(big[nt], ah, uh[g][kb][nt][0], uh[g][kb][nt][1]);
+          mma_bf16(small[nt], al, uh[g][kb][nt][0], uh[g][kb][nt][1]);
+          mma_bf16(small[nt], ah, ul[g][kb][nt][0], ul[g][kb][nt][1]);
         }
       }
-      float4* r0 = reinterpret_cast<float4*>(&sm.u[i0 + gr][c0]);
-      float4* r8 = reinterpret_cast<float4*>(&sm.u[i0 + gr + 8][c0]);
+      float4* r0 = reinterpret_cast<float4*>(&sm.u[i0 + gr][c0(g)]);
+      float4* r8 = reinterpret_cast<float4*>(&sm.u[i0 + gr + 8][c0(g)]);
       const float4 x = *r0, y = *r8;
       auto part = [&](int nt, int e) { return walk ? 0.f : big[nt][e] + small[nt][e]; };
-      *r0 = make_float4(v0.x - x.x - part(0, 0), v0.y - x.y - part(1, 0), v0.z - x.z - part(0, 1), v0.w - x.w - part(1, 1));
+      *r0 = make_float4(v0[g].x - x.x - part(0, 0), v0[g].y - x.y - part(1, 0), v0[g].z - x.z - part(0, 1), v0[g].w - x.w - part(1, 1));
       if (kNodes >= 16)
-        *r8 = make_float4(v8.x - y.x - part(0, 2), v8.y - y.y - part(1, 2), v8.z - y.z - part(0, 3), v8.w - y.w - part(1, 3));
+        *r8 = make_float4(v8[g].x - y.x - part(0, 2), v8[g].y - y.y - part(1, 2), v8[g].z - y.z - part(0, 3), v8[g].w - y.w - part(1, 3));
     }
-    if (blk + 1 < blocks) {
-      v0 = load_quad<kFull>(vs + min(i0 + 16 + gr, n - 1) * row, c0, dv);
-      v8 = load_quad<kFull>(vs + min(i0 + 24 + gr, n - 1) * row, c0, dv);
-    }
+    if (blk + 1 < blocks) load_values(i0 + 16);
     __syncthreads();
     bool odd = false;
     constexpr int kIn = kNodes < 16 ? kNodes : 16;
@@ -391,11 +414,18 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
 #pragma unroll
       for (int i = 0; i < kIn; ++i) r[i] = i0 + i < n ? sm.u[i0 + i][col] : 0.f;
 #pragma unroll
-      for (int j = 0; j < kIn; ++j) {
-        r[j] *= sm.beta[i0 + j];
-        odd |= !isfinite(r[j]);
+      for (int i = 0; i < kIn; ++i) {
+        float s = r[i];
 #pragma unroll
-        for (int i = j + 1; i < kIn; ++i) r[i] = fmaf(-sm.a[i0 + i][i0 + j], r[j], r[i]);
+        for (int j = 0; j < i; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(&sm.a[i0 + i][i0 + j]);
+          s = fmaf(-w.x, r[j], s);
+          if (j + 1 < i) s = fmaf(-w.y, r[j + 1], s);
+          if (j + 2 < i) s = fmaf(-w.z, r[j + 2], s);
+          if (j + 3 < i) s = fmaf(-w.w, r[j + 3], s);
+        }
+        r[i] = s * sm.beta[i0 + i];
+        odd |= !isfinite(r[i]);
       }
     }
     // (what other columns of a row past dv hold is nobody's)
@@ -420,14 +450,18 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
     }
     __syncthreads();
     if (!walk) {
-      const int i = i0 + 4 * q, cc = 16 * warp + 2 * gr;
-      float2 w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = kNodes >= 16 || 4 * q + e < kNodes ? *reinterpret_cast<const float2*>(&sm.u[i + e][cc]) : make_float2(0.f, 0.f);
-      split2(w[0].x, w[1].x, uh[blk][0][0], ul[blk][0][0]);
-      split2(w[2].x, w[3].x, uh[blk][0][1], ul[blk][0][1]);
-      split2(w[0].y, w[1].y, uh[blk][1][0], ul[blk][1][0]);
-      split2(w[2].y, w[3].y, uh[blk][1][1], ul[blk][1][1]);
+      for (int g = 0; g < kCols; ++g) {
+        const int i = i0 + 4 * q, cc = 16 * (warp + kWarps * g) + 2 * gr;
+        float2 w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = kNodes >= 16 || 4 * q + e < kNodes ? *reinterpret_cast<const float2*>(&sm.u[i + e][cc]) : make_float2(0.f, 0.f);
+        split2(w[0].x, w[1].x, uh[g][blk][0][0], ul[g][blk][0][0]);
+        split2(w[2].x, w[3].x, uh[g][blk][0][1], ul[g][blk][0][1]);
+        split2(w[0].y, w[1].y, uh[g][blk][1][0], ul[g][blk][1][0]);
+        split2(w[2].y, w[3].y, uh[g][blk][1][1], ul[g][blk][1][1]);
+      }
     }
   }
   // ---- outputs: (Q o e^G) S plus the scores' product with the deltas
@@ -436,34 +470,37 @@ __global__ void __launch_bounds__(kThreads, kNodes <= 32 ? 2 : 1) tree_kernel(co
     for (int blk = 0; blk < kBlocks; ++blk) {
       if (blk >= blocks) break;
       const int i0 = 16 * blk;
-      float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
-      for (int kb = 0; kb <= blk; ++kb) {
-        uint32_t bh[4], bl[4];
-        split_scores(&sm.b[i0 + gr][16 * kb + 4 * q], &sm.b[i0 + gr + 8][16 * kb + 4 * q], bh, bl);
+      for (int g = 0; g < kCols; ++g) {
+        float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          mma_bf16(big[nt], bh, uh[kb][nt][0], uh[kb][nt][1]);
-          mma_bf16(small[nt], bl, uh[kb][nt][0], uh[kb][nt][1]);
-          mma_bf16(small[nt], bh, ul[kb][nt][0], ul[kb][nt][1]);
+        for (int kb = 0; kb <= blk; ++kb) {
+          uint32_t bh[4], bl[4];
+          split_scores(&sm.b[i0 + gr][16 * kb + 4 * q], &sm.b[i0 + gr + 8][16 * kb + 4 * q], bh, bl);
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            mma_bf16(big[nt], bh, uh[g][kb][nt][0], uh[g][kb][nt][1]);
+            mma_bf16(small[nt], bl, uh[g][kb][nt][0], uh[g][kb][nt][1]);
+            mma_bf16(small[nt], bh, ul[g][kb][nt][0], ul[g][kb][nt][1]);
+          }
         }
-      }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = i0 + gr + 8 * half;
-        if (i < n) {
-          const float4 x = *reinterpret_cast<const float4*>(&sm.qs[i][c0]);
-          const float o[4] = {x.x + big[0][2 * half] + small[0][2 * half], x.y + big[1][2 * half] + small[1][2 * half],
-                              x.z + big[0][2 * half + 1] + small[0][2 * half + 1],
-                              x.w + big[1][2 * half + 1] + small[1][2 * half + 1]};
-          const size_t at = ((size_t)(m0 + i) * p.Hv + h) * dv + c0;
-          if (kFull && wide_out) {
-            if (p.out_bf16) glr::store4(reinterpret_cast<__nv_bfloat16*>(p.out) + at, make_float2(o[0], o[1]), make_float2(o[2], o[3]));
-            else glr::store4(reinterpret_cast<float*>(p.out) + at, make_float2(o[0], o[1]), make_float2(o[2], o[3]));
-          } else {
+        for (int half = 0; half < 2; ++half) {
+          const int i = i0 + gr + 8 * half;
+          if (i < n) {
+            const float4 x = *reinterpret_cast<const float4*>(&sm.qs[i][c0(g)]);
+            const float o[4] = {x.x + big[0][2 * half] + small[0][2 * half], x.y + big[1][2 * half] + small[1][2 * half],
+                                x.z + big[0][2 * half + 1] + small[0][2 * half + 1],
+                                x.w + big[1][2 * half + 1] + small[1][2 * half + 1]};
+            const size_t at = ((size_t)(m0 + i) * p.Hv + h) * dv + c0(g);
+            if (kFull && wide_out) {
+              if (p.out_bf16) glr::store4(reinterpret_cast<__nv_bfloat16*>(p.out) + at, make_float2(o[0], o[1]), make_float2(o[2], o[3]));
+              else glr::store4(reinterpret_cast<float*>(p.out) + at, make_float2(o[0], o[1]), make_float2(o[2], o[3]));
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (c0 + e < dv) store_out(p.out, at + e, o[e], p.out_bf16);
+              for (int e = 0; e < 4; ++e)
+                if (c0(g) + e < dv) store_out(p.out, at + e, o[e], p.out_bf16);
+            }
           }
         }
       }
@@ -580,12 +617,12 @@ __global__ void __launch_bounds__(kThreads, 2) commit_kernel(const TreeArgs p) {
 }
 
 template <typename Kernel, typename... More>
-cudaError_t launch(Kernel kernel, const TreeArgs& a, size_t smem, cudaStream_t stream, More... more) {
+cudaError_t launch(Kernel kernel, const TreeArgs& a, int threads, size_t smem, cudaStream_t stream, More... more) {
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)((int64_t)a.batch * a.Hv), kThreads, smem, stream>>>(a, more...);
+  kernel<<<(unsigned)((int64_t)a.batch * a.Hv), threads, smem, stream>>>(a, more...);
   return cudaGetLastError();
 }
 
@@ -595,12 +632,12 @@ cudaError_t pick(const TreeArgs& a, cudaStream_t stream) {
   const bool full = a.dk == 128 && a.dv == 128 && on(a.pool, 16);
   const size_t smem = kCommit ? sizeof(CommitSmem<kNodes>) : sizeof(TreeSmem<kNodes>);
   if constexpr (kCommit) {
-    auto go = [&](auto kernel) { return launch(kernel, a, smem, stream); };
+    auto go = [&](auto kernel) { return launch(kernel, a, kThreads, smem, stream); };
     if (a.v_first) return full ? go(commit_kernel<kNodes, true, true>) : go(commit_kernel<kNodes, true, false>);
     return full ? go(commit_kernel<kNodes, false, true>) : go(commit_kernel<kNodes, false, false>);
   } else {
     const bool wide_out = on(a.out, a.out_bf16 ? 8 : 16);
-    auto go = [&](auto kernel) { return launch(kernel, a, smem, stream, wide_out); };
+    auto go = [&](auto kernel) { return launch(kernel, a, kTreeThreads<kNodes>, smem, stream, wide_out); };
     using bf16 = __nv_bfloat16;
     // the form for 128 x 128 states reads rows in wide accesses: all of them start on 16 bytes (bf16: 8)
     const size_t in = a.in_bf16 ? 8 : 16;
