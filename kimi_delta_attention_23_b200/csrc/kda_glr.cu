@@ -307,12 +307,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
         g0 = clamp2(g0, gate.lb2);
         g1 = clamp2(g1, gate.lb2);
       }
-      k.a0[r] = make_float2(ex2(g0.x), ex2(g0.y));
-      k.a1[r] = make_float2(ex2(g1.x), ex2(g1.y));
+      const Decay e0 = decay_of(g0), e1 = decay_of(g1);
+      k.a0[r] = e0.a;
+      k.a1[r] = e1.a;
       k.b0[r] = mul2(x0, both(bt_r));
       k.b1[r] = mul2(x1, both(bt_r));
       if constexpr (kNorm) {
-        const float2 u0 = one_minus_sq(g0, k.a0[r]), u1 = one_minus_sq(g1, k.a1[r]);
+        const float2 u0 = one_minus_sq(e0), u1 = one_minus_sq(e1);
         k.b0[r] = mul2(k.b0[r], mul2(u0, rsq2(u0)));
         k.b1[r] = mul2(k.b1[r], mul2(u1, rsq2(u1)));
       }
@@ -588,11 +589,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       float2 g0[kBwdRows], g1[kBwdRows];  // gates (log2), clamped, and finite
       float bt;
     };
-    auto decay = [&](float2 g) { return make_float2(ex2(g.x), ex2(g.y)); };
-    auto input = [&](float2 x, float bt, float2 g, float2 a) {
+    auto input = [&](float2 x, float bt, const Decay& e) {
       float2 in = mul2(x, both(bt));
       if constexpr (kNorm) {
-        const float2 u = one_minus_sq(g, a);
+        const float2 u = one_minus_sq(e);
         in = mul2(in, mul2(u, rsq2(u)));
       }
       return in;
@@ -624,9 +624,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         z1 = pre_log2(z1, bias1);
         k.g0[r] = clamp2(gate_log2(z0, exp_neg_abs(z0), gate.c), fmaxf(gate.lb2, kLeast));
         k.g1[r] = clamp2(gate_log2(z1, exp_neg_abs(z1), gate.c), fmaxf(gate.lb2, kLeast));
-        a0[r] = decay(k.g0[r]);
-        a1[r] = decay(k.g1[r]);
-        float2 b0 = input(x0, bt_r, k.g0[r], a0[r]), b1 = input(x1, bt_r, k.g1[r], a1[r]);
+        const Decay d0 = decay_of(k.g0[r]), d1 = decay_of(k.g1[r]);
+        a0[r] = d0.a;
+        a1[r] = d1.a;
+        float2 b0 = input(x0, bt_r, d0), b1 = input(x1, bt_r, d1);
         if (r >= left) {  // rows past the end are the identity
           a0[r] = a1[r] = one;
           b0 = b1 = zero;
@@ -685,9 +686,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const float bt_r = __shfl_sync(0xffffffffu, k.bt, r);
           float2 x0, x1;
           unpack4(xs + r * pitch, x0, x1);
-          const float2 a0 = decay(k.g0[r]), a1 = decay(k.g1[r]);
-          h0 = fma2(a0, h0, input(x0, bt_r, k.g0[r], a0));
-          h1 = fma2(a1, h1, input(x1, bt_r, k.g1[r], a1));
+          const Decay d0 = decay_of(k.g0[r]), d1 = decay_of(k.g1[r]);
+          h0 = fma2(d0.a, h0, input(x0, bt_r, d0));
+          h1 = fma2(d1.a, h1, input(x1, bt_r, d1));
         }
       }
       float dots[kBwdRows];
@@ -701,7 +702,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         unpack4(raws + r * pitch, z0, z1);
         unpack4(xs + r * pitch, x0, x1);
         unpack4(douts + r * pitch, D0, D1);
-        const float2 a0 = decay(k.g0[r]), a1 = decay(k.g1[r]);
+        const Decay d0 = decay_of(k.g0[r]), d1 = decay_of(k.g1[r]);
+        const float2 a0 = d0.a, a1 = d1.a;
         D0 = add2(D0, back0);
         D1 = add2(D1, back1);
         back0 = mul2(a0, D0);
@@ -710,7 +712,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         float2 xs0 = mul2(D0, x0), xs1 = mul2(D1, x1);                  // D x, times s for dbeta
         float2 dx0 = mul2(D0, both(bt_r)), dx1 = mul2(D1, both(bt_r));
         if constexpr (kNorm) {
-          const float2 u0 = one_minus_sq(k.g0[r], a0), u1 = one_minus_sq(k.g1[r], a1);
+          const float2 u0 = one_minus_sq(d0), u1 = one_minus_sq(d1);
           const float2 i0 = rsq2(u0), i1 = rsq2(u1), s0v = mul2(u0, i0), s1v = mul2(u1, i1);
           // ds/dg = -a^2 / s
           dg0 = fma2(mul2(xs0, both(-bt_r)), mul2(mul2(a0, a0), i0), dg0);
@@ -867,13 +869,13 @@ __global__ void __launch_bounds__(kDecThreads) glr_decode_kernel(const GlrArgs p
   const float bt = beta_f32(p.beta[bh], p.flags & KDA_BETA_PROB);
   auto step = [&](float2 s, float2 xv, float2 z) {
     const float2 g = clamp2(gate_log2(z, exp_neg_abs(z), gate.c), gate.lb2);
-    const float2 a = make_float2(ex2(g.x), ex2(g.y));
+    const Decay e = decay_of(g);
     float2 in = mul2(xv, both(bt));
     if (p.flags & KDA_INPUT_NORM) {
-      const float2 u = one_minus_sq(g, a);
+      const float2 u = one_minus_sq(e);
       in = mul2(in, mul2(u, rsq2(u)));
     }
-    return fma2(a, s, in);
+    return fma2(e.a, s, in);
   };
   s0 = step(s0, x0, pre_log2(z0, mul2(v0, both(kLog2e))));
   if constexpr (kPer == 4) {

@@ -2,7 +2,7 @@
 //
 // The forward pass at HBM speed has about 13 issue slots and 6 MUFU cycles per element and SM
 // sub-core to spend, so the gate is evaluated two channels at a time (fma.rn.f32x2 and friends)
-// with two MUFU operations per element: e = 2^(-|z| log2 e) and a = 2^(g log2 e).  softplus(z) =
+// with two MUFU operations per element: e = 2^(-|z| log2 e) and a = 2^(g log2 e) (a polynomial where a is near 1).  softplus(z) =
 // max(z, 0) + log1p(e) takes log1p as e times a degree-7 polynomial: a logarithm of the rounded
 // 1 + e would lose the gates of slow channels (softplus << 1), whose decays multiply up over
 // thousands of tokens.
@@ -75,13 +75,13 @@ __device__ __forceinline__ float2 log2_1p_ratio(float2 e) {
   return fma2(p, e, both(1.44269478f));
 }
 
-// (1 - exp(-t)) / t for t in [0, 1/2] (relative error 1.5e-7)
-__device__ __forceinline__ float2 one_minus_exp_ratio(float2 t) {
+// (exp(y) - 1) / y for y in [-1/2, 0] (relative error 1.5e-7)
+__device__ __forceinline__ float2 expm1_ratio(float2 y) {
   float2 p = both(0.00677103736f);
-  p = fma2(p, t, both(-0.0410012789f));
-  p = fma2(p, t, both(0.166548148f));
-  p = fma2(p, t, both(-0.49999249f));
-  return fma2(p, t, both(0.99999994f));
+  p = fma2(p, y, both(0.0410012789f));
+  p = fma2(p, y, both(0.166548148f));
+  p = fma2(p, y, both(0.49999249f));
+  return fma2(p, y, both(0.99999994f));
 }
 
 // What one head's gate needs besides the pre-activation: -exp(a_log), and the safe gate's bound times
@@ -110,13 +110,22 @@ __device__ __forceinline__ float2 clamp2(float2 g2, float lb2) {
   return make_float2(max_nan(g2.x, lb2), max_nan(g2.y, lb2));
 }
 
-// 1 - a^2 for a = 2^g2, at least the smallest normal number: by the polynomial for exp(2 g) - 1 where
-// a^2 >= e^(-1/2), since the difference loses what slow channels are made of there.  A channel that
-// is wide open (a = 1) so lets in 1e-19 of its input, which is nothing, and needs no case of its own.
-__device__ __forceinline__ float2 one_minus_sq(float2 g2, float2 a) {
-  const float2 t = mul2(g2, both(-2.f * kLn2));
-  const float2 near = mul2(t, one_minus_exp_ratio(t));
-  const float2 u = make_float2(t.x < 0.5f ? near.x : fmaf(-a.x, a.x, 1.f), t.y < 0.5f ? near.y : fmaf(-a.y, a.y, 1.f));
+// The decay a = 2^g2 and what it leaves, 1 - a.  Slow channels (a >= e^(-1/2)) take both from the
+// polynomial: the hardware exponential is off by up to 2^-22, of a kind with the tokens' 1 - a there,
+// and thousands of such decays multiply up.
+struct Decay {
+  float2 a, rest;
+};
+__device__ __forceinline__ Decay decay_of(float2 g2) {
+  const float2 y = mul2(g2, both(kLn2)), m = mul2(y, expm1_ratio(y)), far = make_float2(ex2(g2.x), ex2(g2.y));
+  const bool near_x = y.x > -0.5f, near_y = y.y > -0.5f;
+  return {make_float2(near_x ? 1.f + m.x : far.x, near_y ? 1.f + m.y : far.y),
+          make_float2(near_x ? -m.x : 1.f - far.x, near_y ? -m.y : 1.f - far.y)};
+}
+// 1 - a^2, at least the smallest normal number: a channel that is wide open (a = 1) so lets in 1e-19 of
+// its input, which is nothing, and needs no case of its own.
+__device__ __forceinline__ float2 one_minus_sq(const Decay& d) {
+  const float2 u = fma2(d.rest, d.a, d.rest);
   return make_float2(fmaxf(u.x, kTiny), fmaxf(u.y, kTiny));
 }
 __device__ __forceinline__ float2 rsq2(float2 u) { return make_float2(rsq(u.x), rsq(u.y)); }

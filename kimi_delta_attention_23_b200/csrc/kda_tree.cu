@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
         const float2 g1 = glr::clamp2(glr::gate_log2(z1, glr::exp_neg_abs(z1), gate.c), gate.lb2);
         if (m < n) {
           *reinterpret_cast<float4*>(&sm.k[m][c4]) = kv[j];
-          *reinterpret_cast<float4*>(&sm.al[m][c4]) = make_float4(glr::ex2(g0.x), glr::ex2(g0.y), glr::ex2(g1.x), glr::ex2(g1.y));
+          const float2 a0 = glr::decay_of(g0).a, a1 = glr::decay_of(g1).a;
+          *reinterpret_cast<float4*>(&sm.al[m][c4]) = make_float4(a0.x, a0.y, a1.x, a1.y);
         }
       }
     }
