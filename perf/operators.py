@@ -227,6 +227,11 @@ def _run_own(s):
         kept = torch.empty(kda.kda_glr_checkpoint_shape(c["tokens"], c["seqs"], c["heads"], c["d"]), device=DEV)
         out = kda.kda_glr_fwd(s["x"], *params, s["cu"], s["pool"], s["idx"], output_dtype=out_type, checkpoints=kept, **kw)
         grads = kda.kda_glr_bwd(s["dout"], s["x"], *params, s["cu"], kept, s["dfinal"], **kw)
+        if c["out"] == "f32":
+            # the plain form adds the final states' gradients into an fp32 dout, where the next pass on the
+            # same state finds them; the two go on from the same dout only if this does so too
+            last, some = (s["cu"][1:] - 1).clamp_min(0), s["cu"][1:] > s["cu"][:-1]
+            s["dout"].index_add_(0, last, s["dfinal"] * some[:, None, None])
         return {"out": out, "pool": s["pool"], **grads}
     if kind == "tree":
         out, deltas = kda.kda_tree_decode(
