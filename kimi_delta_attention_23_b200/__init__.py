@@ -208,21 +208,39 @@ def _stream(stream, device):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _need(t, name, dtype, shape, dev, index):
-    """The address of a contiguous CUDA tensor of this type and shape on device ``index``."""
+def _need(t, name, dtype, shape, like, index):
+    """The address of a contiguous CUDA tensor of this type and shape on device ``index`` (that of ``like``)."""
     try:
         if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
-    _shape(_dev(t, name, dtype, dev), name, shape)
+    _shape(_dev(t, name, dtype, like.device), name, shape)
     return t.data_ptr()
 
 
-def _where(t, name):
-    """The device of a call's first tensor, and its number."""
-    dev = _dev(t, name).device
-    return dev, dev.index
+def _need_rank(t, name, dtype, rank, like, index):
+    """The same for a tensor of which only the number of dimensions is given; returns its shape and address."""
+    try:
+        shape = t.shape
+        if len(shape) == rank and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            return shape, t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name, dtype, like.device)
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rank} dimension(s)")
+
+
+def _where(t, name, rank):
+    """The device number, shape and address of a call's first tensor, a contiguous CUDA tensor."""
+    try:
+        index, shape = t.get_device(), t.shape
+        if index >= 0 and len(shape) == rank and t.is_contiguous():
+            return index, shape, t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name)
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rank} dimension(s)")
 
 
 def _on_stream(stream, index):

@@ -149,6 +149,7 @@ struct FwdSmem {
   uint64_t full[kStages];               // a tile has arrived
   uint64_t mapped[2], entered[2];       // the warps' maps are there; the states entering them are
   uint64_t tiles_in[2];                 // the tiles' maps have arrived
+  int gave_up;
 };
 
 template <typename TX, typename TR, typename TO, bool kNorm, bool kSafe>
@@ -183,12 +184,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
       sm100::mbar_init(sm100::smem_addr(&sm.tiles_in[s]), 1);
     }
     sm100::fence_mbar_init();
+    sm.gave_up = 0;
   }
   cluster.sync();
   auto wait = [&](uint64_t* bar, int parity) {
     const uint32_t at = sm100::smem_addr(bar);
     if (sm100::mbar_try_wait(at, parity & 1)) return;  // nearly always: a sleeping wait takes longer to say so
-    if (!sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    // one wait that ran out is the CTA's last: its threads then run through to the end
+    volatile int* gave_up = &sm.gave_up;
+    if (*gave_up || sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) return;
+    *gave_up = 1;
+    report(p.status, KDA_ERR_DEVICE_TIMEOUT);
   };
 
   const int pitch = how == kTensor ? d : kRow;  // elements of a tile's row
@@ -424,6 +430,7 @@ struct BwdSmem {
   float rev[kMapBuffers][kBwdWarps][kRow];   // B backwards
   float2 tile_map[2][kMaxRanks][kRow];
   uint64_t full[kStages], mapped[2], entered[2], tiles_in[2], done[2];
+  int gave_up;
 };
 
 template <typename TX, typename TR, typename TO, bool kNorm, bool kSafe>
@@ -471,6 +478,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       sm100::mbar_init(sm100::smem_addr(&sm.done[s]), kBwdWarps);
     }
     sm100::fence_mbar_init();
+    sm.gave_up = 0;
   }
   if (how != kTensor && d < kRow) {  // channels past the head must add nothing to the sums over channels
     for (size_t i = threadIdx.x; i < offsetof(Smem, map) / 16; i += kBwdThreads)
@@ -480,7 +488,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   auto wait = [&](uint64_t* bar, int parity) {
     const uint32_t at = sm100::smem_addr(bar);
     if (sm100::mbar_try_wait(at, parity & 1)) return;  // nearly always: a sleeping wait takes longer to say so
-    if (!sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    // one wait that ran out is the CTA's last: its threads then run through to the end
+    volatile int* gave_up = &sm.gave_up;
+    if (*gave_up || sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) return;
+    *gave_up = 1;
+    report(p.status, KDA_ERR_DEVICE_TIMEOUT);
   };
 
   if (warp >= kBwdWarps) {

@@ -13,10 +13,11 @@
 //  1. scores: a group of lanes per node walks from the node to the root.  The decay from the ancestor
 //     to the node is a running product of the tokens' decays (never an exponential of a sum, so
 //     nothing over- or underflows early), which at the root is e^{G_i} itself.
-//  2. P = [K o e^G; Q o e^G] S on mma.sync: S comes from global memory straight into the B
-//     fragments.  Every fp32 factor is split into two bf16 parts and three of the four partial
-//     products are summed (2^-18 of the factors is lost): kda_tree_commit writes the results of this
-//     into fp32 states, which one bf16 product would spoil.
+//  2. P = [K o e^G; Q o e^G] S on mma.sync, S in the B fragments.  kda_tree_commit writes what comes of
+//     this into fp32 states, which single bf16 or tf32 products would spoil, so every fp32 factor is split
+//     into two parts and three of the four partial products are summed.  From fp32 inputs, or where fp32
+//     outputs are asked for, the parts are tf32: 2^-21 of the factors is lost.  Between bf16 inputs and bf16
+//     outputs they are bf16, in half the products: 2^-17 is lost, next to the 2^-9 that v itself has lost.
 //  3. blocks of 16 nodes down the tree: a product with the deltas of the blocks before, then a thread per
 //     value column substitutes within the block; a last product gives the outputs.
 // It is bound by the state's 4 dk dv bytes for drafts of about 16 nodes and fewer.  tcgen05 is not
@@ -25,6 +26,8 @@
 //
 // The commit is S' = e^{G_a} o S + sum over the path (k_j o e^{G_a - G_j}) u_j^T, one pass over the
 // state, bound by its 8 dk dv bytes.
+#include <type_traits>
+
 #include "kda_glr_math.cuh"
 #include "kda_ops_internal.h"
 #include "kda_sm100.cuh"
@@ -35,7 +38,7 @@ namespace {
 constexpr int kThreads = 256;     // of the commit
 constexpr int kPitch = 132;    // floats of a node's row in shared memory
 constexpr uint64_t kWaitNs = 1000000000ull;  // limit of the wait for a copy
-constexpr int kPitchH = 144;   // bf16 of a row of the split factors (32 bytes past 256: no conflicts)
+constexpr int kPitchH = 144;   // elements of a factor's row: 32 (bf16) or 64 (fp32) bytes past a whole line
 
 // Offsets and slot of a sequence; false where one is out of range.
 __device__ __forceinline__ bool tree_at(const TreeArgs& a, int b, int32_t& m0, int32_t& n, int32_t& slot) {
@@ -63,6 +66,18 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo, hi with tf32's 10 bits of mantissa (the hardware does the same to lo: 2^-21 of x is lost)
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
 // x = hi + lo up to 2^-18 of x; two values to a word, the first in the low half
@@ -98,6 +113,7 @@ struct TreeSmem {
     struct {
       __nv_bfloat16 hi[2 * kNodes][kPitchH], lo[2 * kNodes][kPitchH];
     };
+    float factor[2 * kNodes][kPitchH];  // unsplit, where the parts are tf32
   };
   // scores, zero where j is no ancestor of i; the pitch keeps 16-byte reads of neighbouring rows apart
   static constexpr int kRows = kNodes < 16 ? 16 : kNodes;
@@ -124,18 +140,63 @@ __device__ __forceinline__ float4 load_quad(const T* row, int c, int d) {
   }
 }
 
-// The fragments of a 16 x 16 tile of scores in two bf16 parts (rows from smem, the summed index permuted
-// as in the product with the state)
-__device__ __forceinline__ void split_scores(const float* row0, const float* row8, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  const float4 x = *reinterpret_cast<const float4*>(row0), y = *reinterpret_cast<const float4*>(row8);
-  split2(x.x, x.y, hi[0], lo[0]);
-  split2(y.x, y.y, hi[1], lo[1]);
-  split2(x.z, x.w, hi[2], lo[2]);
-  split2(y.z, y.w, hi[3], lo[3]);
+// 16 of the summed index times 8 columns of the right factor: a lane's four elements, 4 (lane % 4) .. + 3 of
+// the summed index, kept as two bf16 parts or as they are.
+template <bool kExact>
+struct Right {
+  uint32_t w[4];  // hi, hi, lo, lo; or four floats
+  __device__ __forceinline__ void set(float s0, float s1, float s2, float s3) {
+    if constexpr (kExact) {
+      w[0] = __float_as_uint(s0), w[1] = __float_as_uint(s1), w[2] = __float_as_uint(s2), w[3] = __float_as_uint(s3);
+    } else {
+      split2(s0, s1, w[0], w[2]);
+      split2(s2, s3, w[1], w[3]);
+    }
+  }
+};
+// 16 rows of the left factor: rows lane / 4 and 8 further, the same four of the summed index
+template <bool kExact>
+struct Left {
+  uint32_t hi[kExact ? 8 : 4], lo[kExact ? 8 : 4];
+  __device__ __forceinline__ void set(float4 x, float4 y) {
+    if constexpr (kExact) {
+      split_tf32(x.x, hi[0], lo[0]), split_tf32(y.x, hi[1], lo[1]), split_tf32(x.y, hi[2], lo[2]), split_tf32(y.y, hi[3], lo[3]);
+      split_tf32(x.z, hi[4], lo[4]), split_tf32(y.z, hi[5], lo[5]), split_tf32(x.w, hi[6], lo[6]), split_tf32(y.w, hi[7], lo[7]);
+    } else {
+      split2(x.x, x.y, hi[0], lo[0]);
+      split2(y.x, y.y, hi[1], lo[1]);
+      split2(x.z, x.w, hi[2], lo[2]);
+      split2(y.z, y.w, hi[3], lo[3]);
+    }
+  }
+};
+// big + small += left right, the large and the small partial products apart
+template <bool kExact>
+__device__ __forceinline__ void multiply(float (&big)[4], float (&small)[4], const Left<kExact>& a, const Right<kExact>& b) {
+  if constexpr (kExact) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t ah[4] = {a.hi[4 * s], a.hi[4 * s + 1], a.hi[4 * s + 2], a.hi[4 * s + 3]};
+      const uint32_t al[4] = {a.lo[4 * s], a.lo[4 * s + 1], a.lo[4 * s + 2], a.lo[4 * s + 3]};
+      uint32_t h0, l0, h1, l1;
+      // (volatile: split anew for every tile of rows; the parts of a whole state do not fit the registers)
+      asm volatile("and.b32 %0, %1, 0xffffe000;" : "=r"(h0) : "r"(b.w[2 * s]));
+      asm volatile("and.b32 %0, %1, 0xffffe000;" : "=r"(h1) : "r"(b.w[2 * s + 1]));
+      l0 = __float_as_uint(__uint_as_float(b.w[2 * s]) - __uint_as_float(h0));
+      l1 = __float_as_uint(__uint_as_float(b.w[2 * s + 1]) - __uint_as_float(h1));
+      mma_tf32(big, ah, h0, h1);
+      mma_tf32(small, al, h0, h1);
+      mma_tf32(small, ah, l0, l1);
+    }
+  } else {
+    mma_bf16(big, a.hi, b.w[0], b.w[1]);
+    mma_bf16(small, a.lo, b.w[0], b.w[1]);
+    mma_bf16(small, a.hi, b.w[2], b.w[3]);
+  }
 }
 
-template <int kNodes, bool kVFirst, bool kFull, typename T>
-__global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNodes <= 32 ? 2 : 1)
+template <int kNodes, bool kVFirst, bool kFull, typename T, bool kExact>
+__global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ? 3 : 4) : kNodes <= 32 ? 2 : 1)
     tree_kernel(const TreeArgs p, const bool wide_out) {
   constexpr int kThreads = kTreeThreads<kNodes>, kWarps = kThreads / 32;
   constexpr int kCols = 8 / kWarps;  // groups of 16 value columns per warp: warp, warp + kWarps, ..
@@ -276,15 +337,22 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
 #pragma unroll
     for (int j = 0; j < kQuads; ++j) {
       const int c = 4 * (g + kGroup * j);
-      uint2 hi, lo;
-      split2(kq[j].x * w[j].x, kq[j].y * w[j].y, hi.x, lo.x);
-      split2(kq[j].z * w[j].z, kq[j].w * w[j].w, hi.y, lo.y);
-      *reinterpret_cast<uint2*>(&sm.hi[rk][c]) = hi;
-      *reinterpret_cast<uint2*>(&sm.lo[rk][c]) = lo;
-      split2(qq[j].x * w[j].x, qq[j].y * w[j].y, hi.x, lo.x);
-      split2(qq[j].z * w[j].z, qq[j].w * w[j].w, hi.y, lo.y);
-      *reinterpret_cast<uint2*>(&sm.hi[rk + 8][c]) = hi;
-      *reinterpret_cast<uint2*>(&sm.lo[rk + 8][c]) = lo;
+      const float4 kf = make_float4(kq[j].x * w[j].x, kq[j].y * w[j].y, kq[j].z * w[j].z, kq[j].w * w[j].w);
+      const float4 qf = make_float4(qq[j].x * w[j].x, qq[j].y * w[j].y, qq[j].z * w[j].z, qq[j].w * w[j].w);
+      if constexpr (kExact) {
+        *reinterpret_cast<float4*>(&sm.factor[rk][c]) = kf;
+        *reinterpret_cast<float4*>(&sm.factor[rk + 8][c]) = qf;
+      } else {
+        uint2 hi, lo;
+        split2(kf.x, kf.y, hi.x, lo.x);
+        split2(kf.z, kf.w, hi.y, lo.y);
+        *reinterpret_cast<uint2*>(&sm.hi[rk][c]) = hi;
+        *reinterpret_cast<uint2*>(&sm.lo[rk][c]) = lo;
+        split2(qf.x, qf.y, hi.x, lo.x);
+        split2(qf.z, qf.w, hi.y, lo.y);
+        *reinterpret_cast<uint2*>(&sm.hi[rk + 8][c]) = hi;
+        *reinterpret_cast<uint2*>(&sm.lo[rk + 8][c]) = lo;
+      }
     }
   }
 
@@ -299,7 +367,7 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
 #pragma unroll 1
   for (int group = warp; group < 8; group += kWarps) {
     const int q = lane & 3, gr = lane >> 2, col = 16 * group + 2 * gr;  // a lane's first column of S
-    uint32_t bh[8][2][2], bl[8][2][2];  // [k-step][n-tile][register]
+    Right<kExact> right[8][2];  // [k-step][n-tile]
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       const int c = 16 * ks + 4 * q;
@@ -324,10 +392,7 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
             s[t][e] = c + e < dk && col + t < dv ? state[state_off(c + e, col + t, dk, dv, kVFirst)] : 0.f;
       }
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        split2(s[t][0], s[t][1], bh[ks][t][0], bl[ks][t][0]);
-        split2(s[t][2], s[t][3], bh[ks][t][1], bl[ks][t][1]);
-      }
+      for (int t = 0; t < 2; ++t) right[ks][t].set(s[t][0], s[t][1], s[t][2], s[t][3]);
     }
     if (group == warp) __syncthreads();  // the factors are there, and a staged state has been read: u and qs take its place
     const int tiles = (n + 7) >> 3;
@@ -336,17 +401,20 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         const int c = 16 * ks + 4 * q;
-        const uint2 h0 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + gr][c]);
-        const uint2 h1 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + gr + 8][c]);
-        const uint2 l0 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + gr][c]);
-        const uint2 l1 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + gr + 8][c]);
-        const uint32_t ah[4] = {h0.x, h1.x, h0.y, h1.y}, al[4] = {l0.x, l1.x, l0.y, l1.y};
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          mma_bf16(big[nt], ah, bh[ks][nt][0], bh[ks][nt][1]);
-          mma_bf16(small[nt], al, bh[ks][nt][0], bh[ks][nt][1]);
-          mma_bf16(small[nt], ah, bl[ks][nt][0], bl[ks][nt][1]);
+        Left<kExact> left;
+        if constexpr (kExact) {
+          left.set(*reinterpret_cast<const float4*>(&sm.factor[16 * t + gr][c]),
+                   *reinterpret_cast<const float4*>(&sm.factor[16 * t + gr + 8][c]));
+        } else {
+          const uint2 h0 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + gr][c]);
+          const uint2 h1 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + gr + 8][c]);
+          const uint2 l0 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + gr][c]);
+          const uint2 l1 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + gr + 8][c]);
+          left.hi[0] = h0.x, left.hi[1] = h1.x, left.hi[2] = h0.y, left.hi[3] = h1.y;
+          left.lo[0] = l0.x, left.lo[1] = l1.x, left.lo[2] = l0.y, left.lo[3] = l1.y;
         }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) multiply<kExact>(big[nt], small[nt], left, right[ks][nt]);
       }
       // accumulator n = 2 (lane % 4) + {0, 1} of tile nt is column 16 warp + 2 n + nt
       const int c0 = 16 * group + 4 * q, i = 8 * t + gr;
@@ -370,7 +438,7 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
   float* deltas = p.deltas + ((size_t)m0 * p.Hv + h) * dv;
   bool walk = false;
   constexpr int kBlocks = (kNodes + 15) / 16;
-  uint32_t uh[kCols][kBlocks][2][2], ul[kCols][kBlocks][2][2];  // solved blocks as fragments: [.][block][n-tile][register]
+  Right<kExact> solved[kCols][kBlocks][2];  // solved blocks as fragments: [.][block][n-tile]
   float4 v0[kCols], v8[kCols];
   auto load_values = [&](int i0) {
 #pragma unroll
@@ -389,14 +457,11 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
       float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
       for (int kb = 0; kb < blk; ++kb) {
-        uint32_t ah[4], al[4];
-        split_scores(&sm.a[i0 + gr][16 * kb + 4 * q], &sm.a[i0 + gr + 8][16 * kb + 4 * q], ah, al);
+        Left<kExact> left;
+        left.set(*reinterpret_cast<const float4*>(&sm.a[i0 + gr][16 * kb + 4 * q]),
+                 *reinterpret_cast<const float4*>(&sm.a[i0 + gr + 8][16 * kb + 4 * q]));
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          mma_bf16(big[nt], ah, uh[g][kb][nt][0], uh[g][kb][nt][1]);
-          mma_bf16(small[nt], al, uh[g][kb][nt][0], uh[g][kb][nt][1]);
-          mma_bf16(small[nt], ah, ul[g][kb][nt][0], ul[g][kb][nt][1]);
-        }
+        for (int nt = 0; nt < 2; ++nt) multiply<kExact>(big[nt], small[nt], left, solved[g][kb][nt]);
       }
       float4* r0 = reinterpret_cast<float4*>(&sm.u[i0 + gr][c0(g)]);
       float4* r8 = reinterpret_cast<float4*>(&sm.u[i0 + gr + 8][c0(g)]);
@@ -458,10 +523,8 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           w[e] = kNodes >= 16 || 4 * q + e < kNodes ? *reinterpret_cast<const float2*>(&sm.u[i + e][cc]) : make_float2(0.f, 0.f);
-        split2(w[0].x, w[1].x, uh[g][blk][0][0], ul[g][blk][0][0]);
-        split2(w[2].x, w[3].x, uh[g][blk][0][1], ul[g][blk][0][1]);
-        split2(w[0].y, w[1].y, uh[g][blk][1][0], ul[g][blk][1][0]);
-        split2(w[2].y, w[3].y, uh[g][blk][1][1], ul[g][blk][1][1]);
+        solved[g][blk][0].set(w[0].x, w[1].x, w[2].x, w[3].x);
+        solved[g][blk][1].set(w[0].y, w[1].y, w[2].y, w[3].y);
       }
     }
   }
@@ -476,14 +539,11 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
         float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
         for (int kb = 0; kb <= blk; ++kb) {
-          uint32_t bh[4], bl[4];
-          split_scores(&sm.b[i0 + gr][16 * kb + 4 * q], &sm.b[i0 + gr + 8][16 * kb + 4 * q], bh, bl);
+          Left<kExact> left;
+          left.set(*reinterpret_cast<const float4*>(&sm.b[i0 + gr][16 * kb + 4 * q]),
+                   *reinterpret_cast<const float4*>(&sm.b[i0 + gr + 8][16 * kb + 4 * q]));
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            mma_bf16(big[nt], bh, uh[g][kb][nt][0], uh[g][kb][nt][1]);
-            mma_bf16(small[nt], bl, uh[g][kb][nt][0], uh[g][kb][nt][1]);
-            mma_bf16(small[nt], bh, ul[g][kb][nt][0], ul[g][kb][nt][1]);
-          }
+          for (int nt = 0; nt < 2; ++nt) multiply<kExact>(big[nt], small[nt], left, solved[g][kb][nt]);
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -639,16 +699,18 @@ cudaError_t pick(const TreeArgs& a, cudaStream_t stream) {
   } else {
     const bool wide_out = on(a.out, a.out_bf16 ? 8 : 16);
     auto go = [&](auto kernel) { return launch(kernel, a, kTreeThreads<kNodes>, smem, stream, wide_out); };
-    using bf16 = __nv_bfloat16;
     // the form for 128 x 128 states reads rows in wide accesses: all of them start on 16 bytes (bf16: 8)
     const size_t in = a.in_bf16 ? 8 : 16;
     const bool wide = full && on(a.q, in) && on(a.k, in) && on(a.v, in) && on(a.raw_gate, 16) && on(a.dt_bias, 16);
-    if (a.in_bf16) {
-      if (a.v_first) return wide ? go(tree_kernel<kNodes, true, true, bf16>) : go(tree_kernel<kNodes, true, false, bf16>);
-      return wide ? go(tree_kernel<kNodes, false, true, bf16>) : go(tree_kernel<kNodes, false, false, bf16>);
-    }
-    if (a.v_first) return wide ? go(tree_kernel<kNodes, true, true, float>) : go(tree_kernel<kNodes, true, false, float>);
-    return wide ? go(tree_kernel<kNodes, false, true, float>) : go(tree_kernel<kNodes, false, false, float>);
+    auto layout = [&](auto type, auto exact) {
+      using T = decltype(type);
+      constexpr bool kExact = decltype(exact)::value;
+      if (a.v_first)
+        return wide ? go(tree_kernel<kNodes, true, true, T, kExact>) : go(tree_kernel<kNodes, true, false, T, kExact>);
+      return wide ? go(tree_kernel<kNodes, false, true, T, kExact>) : go(tree_kernel<kNodes, false, false, T, kExact>);
+    };
+    if (!a.in_bf16) return layout(float{}, std::true_type{});
+    return a.out_bf16 ? layout(__nv_bfloat16{}, std::false_type{}) : layout(__nv_bfloat16{}, std::true_type{});
   }
 }
 

@@ -19,8 +19,7 @@ import ctypes
 
 import torch
 
-from . import (_DTYPES, KdaError, _dev, _flags, _need, _on_device, _on_stream, _used_on, _where,
-               load_library)
+from . import (_DTYPES, KdaError, _dev, _flags, _need, _need_rank, _on_device, _on_stream, _used_on, _where, load_library)
 
 __all__ = ["kda_glr_fwd", "kda_glr_bwd", "kda_glr_decode", "kda_glr_checkpoint_shape", "kda_glr_bwd_workspace_size"]
 
@@ -63,53 +62,48 @@ def _glr_flags(gate_mode, beta_mode, input_mode):
 
 
 def _inputs(x, raw_gate, beta_logits, a_log, dt_bias):
-    """Checks what all three calls read; returns the device, its number, x's shape and the addresses."""
-    dev, index = _where(x, "x")
-    if x.dtype not in _DTYPES:
+    """Checks what all three calls read; returns the device's number, x's shape and the addresses."""
+    index, (T, H, d), xs = _where(x, "x", 3)
+    dtype, gate_dtype = x.dtype, getattr(raw_gate, "dtype", None)
+    if dtype not in _DTYPES:
         raise ValueError("x must be float32 or bfloat16")
-    if x.dim() != 3:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [tokens, heads, d]")
-    T, H, d = x.shape
-    gate_dtype = getattr(raw_gate, "dtype", None)
-    if gate_dtype not in _DTYPES or (x.dtype == torch.float32 and gate_dtype != torch.float32):
-        _dev(raw_gate, "raw_gate", None, dev)
+    if gate_dtype not in _DTYPES or (dtype is torch.float32 and gate_dtype is not torch.float32):
+        _dev(raw_gate, "raw_gate", None, x.device)
         raise ValueError("raw_gate must be float32, or bfloat16 beside a bfloat16 x")
-    return dev, index, T, H, d, (x.data_ptr(), _DTYPES[x.dtype],
-                                 _need(raw_gate, "raw_gate", gate_dtype, (T, H, d), dev, index), _DTYPES[gate_dtype],
-                                 _need(beta_logits, "beta_logits", torch.float32, (T, H), dev, index),
-                                 _need(a_log, "a_log", torch.float32, (H,), dev, index),
-                                 _need(dt_bias, "dt_bias", torch.float32, (H, d), dev, index))
+    return index, T, H, d, (xs, _DTYPES[dtype], _need(raw_gate, "raw_gate", gate_dtype, (T, H, d), x, index),
+                            _DTYPES[gate_dtype], _need(beta_logits, "beta_logits", torch.float32, (T, H), x, index),
+                            _need(a_log, "a_log", torch.float32, (H,), x, index),
+                            _need(dt_bias, "dt_bias", torch.float32, (H, d), x, index))
 
 
-def _offsets(cu_seqlens, dev, index):
-    _dev(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+def _offsets(cu_seqlens, like, index):
+    (count,), at = _need_rank(cu_seqlens, "cu_seqlens", torch.int32, 1, like, index)
+    if count < 1:
         raise ValueError("cu_seqlens must hold B + 1 offsets")
-    return cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+    return count - 1, at
 
 
-def _pool(state_pool, state_indices, dev, index, B, H, d):
-    _dev(state_pool, "state_pool", torch.float32, dev)
-    if state_pool.dim() != 3 or state_pool.shape[1] != H or state_pool.shape[2] != d:
-        raise ValueError(f"state_pool has shape {tuple(state_pool.shape)}, expected [slots, {H}, {d}]")
-    return (state_pool.data_ptr(), state_pool.shape[0],
-            _need(state_indices, "state_indices", torch.int32, (B,), dev, index))
+def _pool(state_pool, state_indices, like, index, B, H, d):
+    shape, at = _need_rank(state_pool, "state_pool", torch.float32, 3, like, index)
+    if shape[1] != H or shape[2] != d:
+        raise ValueError(f"state_pool has shape {tuple(shape)}, expected [slots, {H}, {d}]")
+    return at, shape[0], _need(state_indices, "state_indices", torch.int32, (B,), like, index)
 
 
-def _output(out, output_dtype, x, dev, index):
+def _output(out, output_dtype, x, index):
     """The output (made here if ``out`` is None), its address and type."""
     if output_dtype is None:
         output_dtype = x.dtype if out is None else out.dtype
-    if output_dtype not in _DTYPES or (x.dtype == torch.float32 and output_dtype != torch.float32):
+    if output_dtype not in _DTYPES or (x.dtype is torch.float32 and output_dtype is not torch.float32):
         raise ValueError("output_dtype must be float32, or bfloat16 beside a bfloat16 x")
     if out is None:
         out = torch.empty_like(x, dtype=output_dtype)
         return out, out.data_ptr(), _DTYPES[output_dtype]
-    return out, _need(out, "out", output_dtype, x.shape, dev, index), _DTYPES[output_dtype]
+    return out, _need(out, "out", output_dtype, x.shape, x, index), _DTYPES[output_dtype]
 
 
-def _status(device_status, dev, index):
-    return None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
+def _status(device_status, like, index):
+    return None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), like, index)
 
 
 def kda_glr_fwd(x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices, out=None, *,
@@ -123,15 +117,15 @@ def kda_glr_fwd(x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool
     ``checkpoints`` (f32, kda_glr_checkpoint_shape(T, B, H, d)) keeps what kda_glr_bwd needs.
     """
     lib = load_library()
-    dev, index, T, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
-    B, cu = _offsets(cu_seqlens, dev, index)
-    pool, slots, indices = _pool(state_pool, state_indices, dev, index, B, H, d)
+    index, T, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    B, cu = _offsets(cu_seqlens, x, index)
+    pool, slots, indices = _pool(state_pool, state_indices, x, index, B, H, d)
     kept = None
     if checkpoints is not None:
-        kept = _need(checkpoints, "checkpoints", torch.float32, (lib.kda_glr_checkpoints(T, B), H, d), dev, index)
-    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, dev, index)
+        kept = _need(checkpoints, "checkpoints", torch.float32, (lib.kda_glr_checkpoints(T, B), H, d), x, index)
+    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, x, index)
     given = out
-    out, to, out_type = _output(out, output_dtype, x, dev, index)
+    out, to, out_type = _output(out, output_dtype, x, index)
     with _on_device(index):
         rc = lib.kda_glr_fwd(*inputs, cu, B, T, H, d, pool, slots, indices, to, out_type, kept, flags, gate_lower_bound,
                              status, _on_stream(stream, index))
@@ -147,11 +141,11 @@ def kda_glr_decode(x, raw_gate, beta_logits, a_log, dt_bias, state_pool, state_i
                    device_status=None, stream=None):
     """One token of each sequence: x, raw_gate [B,H,d]; beta_logits [B,H]; the rest as kda_glr_fwd."""
     lib = load_library()
-    dev, index, B, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
-    pool, slots, indices = _pool(state_pool, state_indices, dev, index, B, H, d)
-    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, dev, index)
+    index, B, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    pool, slots, indices = _pool(state_pool, state_indices, x, index, B, H, d)
+    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, x, index)
     given = out
-    out, to, out_type = _output(out, output_dtype, x, dev, index)
+    out, to, out_type = _output(out, output_dtype, x, index)
     with _on_device(index):
         rc = lib.kda_glr_decode(*inputs, B, H, d, pool, slots, indices, to, out_type, flags, gate_lower_bound, status,
                                 _on_stream(stream, index))
@@ -177,24 +171,24 @@ def kda_glr_bwd(dout, x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, chec
     allocated when not given.
     """
     lib = load_library()
-    dev, index, T, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+    index, T, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
     dtype = getattr(dout, "dtype", None)
     if dtype not in _DTYPES or (x.dtype == torch.float32 and dtype != torch.float32):
-        _dev(dout, "dout", None, dev)
+        _dev(dout, "dout", None, x.device)
         raise ValueError("dout must be float32, or bfloat16 beside a bfloat16 x")
-    douts = _need(dout, "dout", dtype, (T, H, d), dev, index)
-    B, cu = _offsets(cu_seqlens, dev, index)
-    kept = _need(checkpoints, "checkpoints", torch.float32, (lib.kda_glr_checkpoints(T, B), H, d), dev, index)
-    final = None if d_final is None else _need(d_final, "d_final", torch.float32, (B, H, d), dev, index)
-    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, dev, index)
+    douts = _need(dout, "dout", dtype, (T, H, d), x, index)
+    B, cu = _offsets(cu_seqlens, x, index)
+    kept = _need(checkpoints, "checkpoints", torch.float32, (lib.kda_glr_checkpoints(T, B), H, d), x, index)
+    final = None if d_final is None else _need(d_final, "d_final", torch.float32, (B, H, d), x, index)
+    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, x, index)
     made = []
 
     def grad(t, name, shape, dtype=torch.float32):
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
+            t = torch.empty(shape, dtype=dtype, device=x.device)
             made.append(t)
             return t, t.data_ptr()
-        return t, _need(t, name, dtype, shape, dev, index)
+        return t, _need(t, name, dtype, shape, x, index)
 
     dx, dxs = grad(dx, "dx", (T, H, d), x.dtype)
     draw_gate, draws = grad(draw_gate, "draw_gate", (T, H, d), raw_gate.dtype)
@@ -204,9 +198,9 @@ def kda_glr_bwd(dout, x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, chec
     d_initial, dis = grad(d_initial, "d_initial", (B, H, d))
     with _on_device(index):
         if workspace is None:
-            workspace = torch.empty(lib.kda_glr_bwd_workspace_size(T, B, H, d), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(lib.kda_glr_bwd_workspace_size(T, B, H, d), dtype=torch.uint8, device=x.device)
             made.append(workspace)
-        _dev(workspace, "workspace", torch.uint8, dev)
+        _dev(workspace, "workspace", torch.uint8, x.device)
         rc = lib.kda_glr_bwd(douts, _DTYPES[dtype], *inputs, cu, B, T, H, d, kept, final, dxs, draws, dbetas, das, dbs, dis,
                              flags, gate_lower_bound, workspace.data_ptr(), workspace.numel(), status,
                              _on_stream(stream, index))

@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import KdaError, _dev, _need, _on_device, _on_stream, _used_on, load_library
+from . import KdaError, _dev, _need, _need_rank, _on_device, _on_stream, _used_on, load_library
 
 __all__ = ["kda_pool_copy", "kda_pool_fork", "kda_pool_free", "kda_pool_compact", "kda_pool_workspace_size",
            "MAX_POOL_COPIES"]
@@ -36,38 +36,37 @@ def kda_pool_workspace_size(n, max_slots) -> int:
 
 
 def _layout(pool, stacked):
-    _dev(pool, "state_pool", torch.float32)
-    shape, lead = pool.shape, 2 if stacked else 1
-    if len(shape) < lead + 1 or pool.numel() == 0:
+    """The pool itself, its device's number, and its layers, slots and elements per slot."""
+    shape, lead = getattr(pool, "shape", ()), 2 if stacked else 1
+    if len(shape) <= lead or pool.dtype is not torch.float32 or not pool.is_cuda or not pool.is_contiguous() or not pool.numel():
+        _dev(pool, "state_pool", torch.float32)
         raise ValueError(f"state_pool has shape {tuple(shape)}, expected "
                          f"{'[layers, slots, ...]' if stacked else '[slots, ...]'} with at least one element")
     layers, slots = (shape[0], shape[1]) if stacked else (1, shape[0])
-    return pool.device, layers, slots, pool.numel() // (layers * slots)
+    return pool, pool.get_device(), layers, slots, pool.numel() // (layers * slots)
 
 
-def _list(t, name, dev, n=None):
+def _list(t, name, pool, index, n=None):
     """The length and address of a list of slots."""
     if n is not None:
-        return n, _need(t, name, torch.int32, (n,), dev, dev.index)
-    _dev(t, name, torch.int32, dev)
-    if t.dim() != 1:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected one dimension")
-    return t.numel(), t.data_ptr()
+        return n, _need(t, name, torch.int32, (n,), pool, index)
+    (n,), at = _need_rank(t, name, torch.int32, 1, pool, index)
+    return n, at
 
 
 def _call(what, pool, layout, lists, n, results, workspace, device_status, stream, made=()):
-    dev, layers, slots, elems = layout
-    index, lib = dev.index, load_library()
-    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
+    _, index, layers, slots, elems = layout
+    lib = load_library()
+    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), pool, index)
     with _on_device(index):
         if workspace is None and what == "kda_pool_copy" and n <= FEW_COPIES:
             at, size = None, 0
         elif workspace is None:
-            workspace = torch.empty(lib.kda_pool_workspace_size(n, slots), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(lib.kda_pool_workspace_size(n, slots), dtype=torch.uint8, device=pool.device)
             made = (*made, workspace)
             at, size = workspace.data_ptr(), workspace.numel()
         else:
-            _dev(workspace, "workspace", torch.uint8, dev)
+            _dev(workspace, "workspace", torch.uint8, pool.device)
             at, size = workspace.data_ptr(), workspace.numel()
         rc = getattr(lib, what)(pool.data_ptr(), layers, slots, elems, *lists, n, *results, at, size, status,
                                 _on_stream(stream, index))
@@ -82,9 +81,9 @@ def kda_pool_copy(state_pool, src, dst, *, stacked=False, workspace=None, device
     ``src``, ``dst`` [n] i32, n <= 8192.  Slots out of range, and a destination that is named again
     (its first pair counts), are reported in ``device_status`` and skipped.
     """
-    layout = dev, _, _, _ = _layout(state_pool, stacked)
-    n, srcs = _list(src, "src", dev)
-    _, dsts = _list(dst, "dst", dev, n)
+    layout = _, index, _, _, _ = _layout(state_pool, stacked)
+    n, srcs = _list(src, "src", state_pool, index)
+    _, dsts = _list(dst, "dst", state_pool, index, n)
     if n > MAX_POOL_COPIES:
         raise ValueError(f"at most {MAX_POOL_COPIES} pairs per call, got {n}")
     _call("kda_pool_copy", state_pool, layout, (srcs, dsts), n, (), workspace, device_status, stream)
@@ -96,14 +95,14 @@ def kda_pool_fork(state_pool, live, src, dst=None, *, stacked=False, workspace=N
     The lowest free slots are taken in the order of the list.  A source that is not live, or one for
     which no slot is left, is reported in ``device_status`` and gets -1.
     """
-    layout = dev, _, slots, _ = _layout(state_pool, stacked)
-    _, lives = _list(live, "live", dev, slots)
-    n, srcs = _list(src, "src", dev)
+    layout = _, index, _, slots, _ = _layout(state_pool, stacked)
+    _, lives = _list(live, "live", state_pool, index, slots)
+    n, srcs = _list(src, "src", state_pool, index)
     made = ()
     if dst is None:
         dst = torch.empty_like(src)
         made = (dst,)
-    _, dsts = _list(dst, "dst", dev, n)
+    _, dsts = _list(dst, "dst", state_pool, index, n)
     _call("kda_pool_fork", state_pool, layout, (lives, srcs, dsts), n, (), workspace, device_status, stream, made)
     return dst
 
@@ -113,9 +112,9 @@ def kda_pool_free(state_pool, live, slots, *, stacked=False, workspace=None, dev
 
     A slot that is not live, or is listed again, is reported in ``device_status`` and left alone.
     """
-    layout = dev, _, max_slots, _ = _layout(state_pool, stacked)
-    _, lives = _list(live, "live", dev, max_slots)
-    n, listed = _list(slots, "slots", dev)
+    layout = _, index, _, max_slots, _ = _layout(state_pool, stacked)
+    _, lives = _list(live, "live", state_pool, index, max_slots)
+    n, listed = _list(slots, "slots", state_pool, index)
     _call("kda_pool_free", state_pool, layout, (lives, listed), n, (), workspace, device_status, stream)
 
 
@@ -128,13 +127,13 @@ def kda_pool_compact(state_pool, live, state_indices, num_live=None, *, stacked=
     new places; an index that names no live slot is reported in ``device_status`` and kept.  What is
     left in the slots above is unspecified.
     """
-    layout = dev, _, slots, _ = _layout(state_pool, stacked)
-    _, lives = _list(live, "live", dev, slots)
-    n, indices = _list(state_indices, "state_indices", dev)
+    layout = _, index, _, slots, _ = _layout(state_pool, stacked)
+    _, lives = _list(live, "live", state_pool, index, slots)
+    n, indices = _list(state_indices, "state_indices", state_pool, index)
     made = ()
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=dev)
+        num_live = torch.empty(1, dtype=torch.int32, device=state_pool.device)
         made = (num_live,)
-    _, counts = _list(num_live, "num_live", dev, 1)
+    _, counts = _list(num_live, "num_live", state_pool, index, 1)
     _call("kda_pool_compact", state_pool, layout, (lives, indices), n, (counts,), workspace, device_status, stream, made)
     return num_live

@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from . import (_DTYPES, KdaError, _dev, _flags, _need, _on_device, _on_stream, _used_on, _where, load_library)
+from . import _DTYPES, KdaError, _flags, _need, _need_rank, _on_device, _on_stream, _used_on, _where, load_library
 
 __all__ = ["kda_tree_decode", "kda_tree_commit", "MAX_TREE_NODES"]
 
@@ -37,25 +37,23 @@ def _tree_flags(gate_mode, beta_mode, state_layout):
     return _FLAGS[key]
 
 
-def _tree(cu_nodes, parents, max_nodes, M, dev, index):
-    _dev(cu_nodes, "cu_nodes", torch.int32, dev)
-    if cu_nodes.dim() != 1 or cu_nodes.numel() < 1:
+def _tree(cu_nodes, parents, max_nodes, M, like, index):
+    (count,), cu = _need_rank(cu_nodes, "cu_nodes", torch.int32, 1, like, index)
+    if count < 1:
         raise ValueError("cu_nodes must hold B + 1 offsets")
     if max_nodes is None:
         max_nodes = max(1, min(M, MAX_TREE_NODES))
     if not 1 <= max_nodes <= MAX_TREE_NODES:
         raise ValueError(f"max_nodes must be 1 .. {MAX_TREE_NODES}, got {max_nodes}")
-    return (cu_nodes.numel() - 1, int(max_nodes), cu_nodes.data_ptr(),
-            _need(parents, "parents", torch.int32, (M,), dev, index))
+    return count - 1, int(max_nodes), cu, _need(parents, "parents", torch.int32, (M,), like, index)
 
 
-def _pool(state_pool, state_indices, state_layout, dev, index, B, Hv, dk, dv):
-    blk = (Hv, dk, dv) if state_layout == "K_FIRST" else (Hv, dv, dk)
-    _dev(state_pool, "state_pool", torch.float32, dev)
-    if state_pool.dim() != 4 or state_pool.shape[1:] != blk:
-        raise ValueError(f"state_pool has shape {tuple(state_pool.shape)}, expected [slots, {blk}]")
-    return (state_pool.data_ptr(), state_pool.shape[0],
-            _need(state_indices, "state_indices", torch.int32, (B,), dev, index))
+def _pool(state_pool, state_indices, state_layout, like, index, B, Hv, dk, dv):
+    shape, at = _need_rank(state_pool, "state_pool", torch.float32, 4, like, index)
+    if shape[1:] != ((Hv, dk, dv) if state_layout == "K_FIRST" else (Hv, dv, dk)):
+        raise ValueError(f"state_pool has shape {tuple(shape)}, expected [slots, {Hv}] and blocks of {dk} keys by {dv} "
+                         f"values stored {state_layout}")
+    return at, shape[0], _need(state_indices, "state_indices", torch.int32, (B,), like, index)
 
 
 def kda_tree_decode(q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_nodes, parents, state_pool, state_indices,
@@ -72,30 +70,26 @@ def kda_tree_decode(q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_nodes, pa
     deltas [M,Hv,dv] f32), the second for kda_tree_commit.
     """
     lib = load_library()
-    dev, index = _where(q, "q")
+    index, (M, Hk, dk), qs = _where(q, "q", 3)
     dtype = q.dtype
     if dtype not in _DTYPES:
         raise ValueError("q/k/v must be float32 or bfloat16")
-    if q.dim() != 3:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected [M, Hk, dk]")
-    M, Hk, dk = q.shape
-    ks = _need(k, "k", dtype, (M, Hk, dk), dev, index)
-    _dev(v, "v", dtype, dev)
-    if v.dim() != 3 or v.shape[0] != M:
+    ks = _need(k, "k", dtype, (M, Hk, dk), q, index)
+    (rows, Hv, dv), vs = _need_rank(v, "v", dtype, 3, q, index)
+    if rows != M:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected [{M}, Hv, dv]")
-    _, Hv, dv = v.shape
-    raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), dev, index)
-    betas = _need(beta_logits, "beta_logits", torch.float32, (M, Hv), dev, index)
-    alogs = _need(a_log, "a_log", torch.float32, (Hv,), dev, index)
-    biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), dev, index)
-    B, max_nodes, cu, pars = _tree(cu_nodes, parents, max_nodes, M, dev, index)
+    raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), q, index)
+    betas = _need(beta_logits, "beta_logits", torch.float32, (M, Hv), q, index)
+    alogs = _need(a_log, "a_log", torch.float32, (Hv,), q, index)
+    biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), q, index)
+    B, max_nodes, cu, pars = _tree(cu_nodes, parents, max_nodes, M, q, index)
     flags = _tree_flags(gate_mode, beta_mode, state_layout)
-    pool, slots, indices = _pool(state_pool, state_indices, state_layout, dev, index, B, Hv, dk, dv)
+    pool, slots, indices = _pool(state_pool, state_indices, state_layout, q, index, B, Hv, dk, dv)
     if output_dtype is None:
         output_dtype = v.dtype if out is None else out.dtype
     if output_dtype not in _DTYPES:
         raise ValueError("output_dtype must be float32 or bfloat16")
-    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
+    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), q, index)
     made = []
     if out is None:
         out = torch.empty_like(v, dtype=output_dtype)
@@ -104,10 +98,10 @@ def kda_tree_decode(q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_nodes, pa
         deltas = torch.empty_like(v, dtype=torch.float32)
         made.append(deltas)
     with _on_device(index):
-        rc = lib.kda_tree_decode(q.data_ptr(), ks, v.data_ptr(), _DTYPES[dtype], raws, betas, alogs, biases, cu, pars, B, M,
+        rc = lib.kda_tree_decode(qs, ks, vs, _DTYPES[dtype], raws, betas, alogs, biases, cu, pars, B, M,
                                  max_nodes, Hk, Hv, dk, dv, pool, slots, indices,
-                                 _need(out, "out", output_dtype, (M, Hv, dv), dev, index), _DTYPES[output_dtype],
-                                 _need(deltas, "deltas", torch.float32, (M, Hv, dv), dev, index), flags,
+                                 _need(out, "out", output_dtype, (M, Hv, dv), q, index), _DTYPES[output_dtype],
+                                 _need(deltas, "deltas", torch.float32, (M, Hv, dv), q, index), flags,
                                  gate_lower_bound, status, _on_stream(stream, index))
     _used_on(stream, index, *made)
     if rc != 0:
@@ -124,26 +118,22 @@ def kda_tree_commit(k, raw_gate, a_log, dt_bias, deltas, cu_nodes, parents, acce
     state stays).  The other tensors as in the kda_tree_decode call that returned ``deltas``.
     """
     lib = load_library()
-    dev, index = _where(k, "k")
+    index, (M, Hk, dk), ks = _where(k, "k", 3)
     if k.dtype not in _DTYPES:
         raise ValueError("k must be float32 or bfloat16")
-    if k.dim() != 3:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected [M, Hk, dk]")
-    M, Hk, dk = k.shape
-    _dev(deltas, "deltas", torch.float32, dev)
-    if deltas.dim() != 3 or deltas.shape[0] != M:
+    (rows, Hv, dv), found = _need_rank(deltas, "deltas", torch.float32, 3, k, index)
+    if rows != M:
         raise ValueError(f"deltas has shape {tuple(deltas.shape)}, expected [{M}, Hv, dv]")
-    _, Hv, dv = deltas.shape
-    raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), dev, index)
-    alogs = _need(a_log, "a_log", torch.float32, (Hv,), dev, index)
-    biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), dev, index)
-    B, max_nodes, cu, pars = _tree(cu_nodes, parents, max_nodes, M, dev, index)
-    took = _need(accepted, "accepted", torch.int32, (B,), dev, index)
+    raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), k, index)
+    alogs = _need(a_log, "a_log", torch.float32, (Hv,), k, index)
+    biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), k, index)
+    B, max_nodes, cu, pars = _tree(cu_nodes, parents, max_nodes, M, k, index)
+    took = _need(accepted, "accepted", torch.int32, (B,), k, index)
     flags = _tree_flags(gate_mode, "logits", state_layout)
-    pool, slots, indices = _pool(state_pool, state_indices, state_layout, dev, index, B, Hv, dk, dv)
-    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), dev, index)
+    pool, slots, indices = _pool(state_pool, state_indices, state_layout, k, index, B, Hv, dk, dv)
+    status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), k, index)
     with _on_device(index):
-        rc = lib.kda_tree_commit(k.data_ptr(), _DTYPES[k.dtype], raws, alogs, biases, deltas.data_ptr(), cu, pars, took, B, M,
+        rc = lib.kda_tree_commit(ks, _DTYPES[k.dtype], raws, alogs, biases, found, cu, pars, took, B, M,
                                  max_nodes, Hk, Hv, dk, dv, pool, slots, indices, flags, gate_lower_bound, status,
                                  _on_stream(stream, index))
     if rc != 0:
