@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
   constexpr int kGroup = kThreads / kNodes;  // lanes per node
   constexpr int kQuads = 32 / kGroup;        // float4's of channels per lane
   static_assert(kGroup <= 32 && kQuads >= 1, "");
-  constexpr int kAtOnce = kNodes >= 32 ? 4 : kNodes / kWarps;  // rows of a warp with their loads in flight together
+  constexpr int kAtOnce = kNodes == 64 ? 8 : kNodes >= 32 ? 4 : kNodes / kWarps;  // rows of a warp with their loads in flight together
   const int node = tid / kGroup, g = tid % kGroup;
   const int mine = min(tid, n - 1);
   const int32_t parent = p.parents[m0 + mine];
@@ -364,9 +364,22 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
     if (!sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
   }
   const float* from = kFull && kStaged<kNodes> ? sm.state : state;
+  const int q = lane & 3, gr = lane >> 2;
+  auto c0 = [&](int g) { return 16 * (warp + kWarps * g) + 4 * q; };  // a lane's columns of the products
+  const size_t row = (size_t)p.Hv * dv;
+  const T* vs = reinterpret_cast<const T*>(p.v) + ((size_t)m0 * p.Hv + h) * dv;
+  float4 v0[kCols], v8[kCols];
+  auto load_values = [&](int i0) {
+#pragma unroll
+    for (int g = 0; g < kCols; ++g) {
+      v0[g] = load_quad<kFull>(vs + min(i0 + gr, n - 1) * row, c0(g), dv);
+      v8[g] = load_quad<kFull>(vs + min(i0 + gr + 8, n - 1) * row, c0(g), dv);
+    }
+  };
+  if constexpr (kNodes == 64) load_values(0);  // where the registers allow it, ahead of the products
 #pragma unroll 1
   for (int group = warp; group < 8; group += kWarps) {
-    const int q = lane & 3, gr = lane >> 2, col = 16 * group + 2 * gr;  // a lane's first column of S
+    const int col = 16 * group + 2 * gr;  // a lane's first column of S
     Right<kExact> right[8][2];  // [k-step][n-tile]
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
@@ -430,24 +443,12 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
   // as above), the rest a substitution with a thread per value column.  The products run over all
   // nodes, weights being zero where one is no ancestor; a delta that is not finite must not reach
   // other branches through such a zero, so from the first one on, ancestors are walked instead.
-  const int q = lane & 3, gr = lane >> 2;
-  auto c0 = [&](int g) { return 16 * (warp + kWarps * g) + 4 * q; };  // a lane's columns of the products
   const int blocks = (n + 15) >> 4, col = tid & 127;
-  const size_t row = (size_t)p.Hv * dv;
-  const T* vs = reinterpret_cast<const T*>(p.v) + ((size_t)m0 * p.Hv + h) * dv;
   float* deltas = p.deltas + ((size_t)m0 * p.Hv + h) * dv;
   bool walk = false;
   constexpr int kBlocks = (kNodes + 15) / 16;
   Right<kExact> solved[kCols][kBlocks][2];  // solved blocks as fragments: [.][block][n-tile]
-  float4 v0[kCols], v8[kCols];
-  auto load_values = [&](int i0) {
-#pragma unroll
-    for (int g = 0; g < kCols; ++g) {
-      v0[g] = load_quad<kFull>(vs + min(i0 + gr, n - 1) * row, c0(g), dv);
-      v8[g] = load_quad<kFull>(vs + min(i0 + gr + 8, n - 1) * row, c0(g), dv);
-    }
-  };
-  load_values(0);
+  if constexpr (kNodes < 64) load_values(0);
 #pragma unroll
   for (int blk = 0; blk < kBlocks; ++blk) {
     if (blk >= blocks) break;
@@ -502,7 +503,6 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
 #pragma unroll
         for (int i = 0; i < kIn; ++i) {
           sm.u[i0 + i][col] = r[i];
-          if (i0 + i < n && col < dv) deltas[(i0 + i) * row + col] = r[i];
         }
       } else {
         for (int i = i0; i < min(i0 + 16, n); ++i) {
@@ -510,7 +510,6 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
           for (int j = sm.par[i]; j >= (before ? 0 : i0); j = sm.par[j]) s = fmaf(-sm.a[i][j], sm.u[j][col], s);
           s *= sm.beta[i];
           sm.u[i][col] = s;
-          if (col < dv) deltas[i * row + col] = s;
         }
       }
     }
@@ -528,7 +527,19 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
       }
     }
   }
-  // ---- outputs: (Q o e^G) S plus the scores' product with the deltas
+  // ---- the deltas, and the outputs: (Q o e^G) S plus the scores' product with them
+  for (int i = warp; i < n; i += kWarps) {
+    const float4 x = *reinterpret_cast<const float4*>(&sm.u[i][c4]);
+    float* to = deltas + i * row + c4;
+    if (kFull && wide_out) {
+      *reinterpret_cast<float4*>(to) = x;
+    } else {
+      if (c4 < dv) to[0] = x.x;
+      if (c4 + 1 < dv) to[1] = x.y;
+      if (c4 + 2 < dv) to[2] = x.z;
+      if (c4 + 3 < dv) to[3] = x.w;
+    }
+  }
   if (!walk) {
 #pragma unroll
     for (int blk = 0; blk < kBlocks; ++blk) {
@@ -697,7 +708,7 @@ cudaError_t pick(const TreeArgs& a, cudaStream_t stream) {
     if (a.v_first) return full ? go(commit_kernel<kNodes, true, true>) : go(commit_kernel<kNodes, true, false>);
     return full ? go(commit_kernel<kNodes, false, true>) : go(commit_kernel<kNodes, false, false>);
   } else {
-    const bool wide_out = on(a.out, a.out_bf16 ? 8 : 16);
+    const bool wide_out = on(a.out, a.out_bf16 ? 8 : 16) && on(a.deltas, 16);
     auto go = [&](auto kernel) { return launch(kernel, a, kTreeThreads<kNodes>, smem, stream, wide_out); };
     // the form for 128 x 128 states reads rows in wide accesses: all of them start on 16 bytes (bf16: 8)
     const size_t in = a.in_bf16 ? 8 : 16;
