@@ -100,6 +100,12 @@ struct Map4 {
   float2 a0, a1, b0, b1;
 };
 
+// The forward kernel is launched with 96 registers per thread; its 4 carrying warps leave 32 of theirs to
+// the 16 computing ones: 16 x 104 + 4 x 64 = 20 x 96 (131072 tokens: 1011 -> 903 us).  The backward
+// kernel's carrying warps need what they have.
+constexpr int kLaunchRegs = 96, kComputeRegs = 104, kCarryRegs = 64;
+static_assert(16 * kComputeRegs + 4 * kCarryRegs <= 20 * kLaunchRegs, "more registers than the CTA has");
+
 template <int kId, int kThreads>
 __device__ __forceinline__ void named_barrier_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(kId), "n"(kThreads) : "memory");
@@ -201,6 +207,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
 
   if (warp >= kFwdWarps) {
     // ---------------------------------------------------------------- carrying warps
+    sm100::regs_decrease<kCarryRegs>();
     const int c = threadIdx.x - 32 * kFwdWarps;
     auto fetch = [&](int step) {
       if (how != kTensor || c != 0 || step >= steps) return;
@@ -256,6 +263,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
   }
 
   // ------------------------------------------------------------------ computing warps
+  sm100::regs_increase<kComputeRegs>();
   const HeadGate gate = head_gate(p.a_log[h], kSafe, p.lb);
   const bool prob = p.flags & KDA_BETA_PROB;
   float2 bias0, bias1;
@@ -991,6 +999,11 @@ cudaError_t fwd(const GlrArgs& a, cudaStream_t stream) {
   const bool norm = a.flags & KDA_INPUT_NORM, safe = a.flags & KDA_GATE_SAFE;
   const auto kernel = norm ? (safe ? glr_fwd_kernel<TX, TR, TO, true, true> : glr_fwd_kernel<TX, TR, TO, true, false>)
                            : (safe ? glr_fwd_kernel<TX, TR, TO, false, true> : glr_fwd_kernel<TX, TR, TO, false, false>);
+  // the warps' shares come out of what a CTA is launched with: with less, they would wait for good
+  cudaFuncAttributes built;
+  const cudaError_t e = cudaFuncGetAttributes(&built, kernel);
+  if (e != cudaSuccess) return e;
+  if (built.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
   return launch_cluster(kernel, (unsigned)grid, kFwdThreads, smem, ranks, stream, a, maps, how, out_map, vec_out);
 }
 
