@@ -10,14 +10,19 @@
 //     dx = D beta s,   dbeta = sum_c D s x,   dg = D (a h_{t-1} + beta x ds/da a),   ds/da = -a / s
 //     draw = -dg exp(a_log) sigmoid(z)  (0 where the safe gate is clamped),  da_log = sum dg g
 //
-// Work per element is a few dozen instructions against 6 to 10 bytes, so the passes are bound by
-// HBM as long as every input is read once.  A scan needs no second reading when whoever reads a
-// tile also finishes it: a cluster of CTAs walks along one (sequence, head), each CTA taking every
-// cluster-size-th tile of 64 tokens x d channels.  Inside the CTA a warp holds consecutive tokens
-// (a lane: four channels), reduces them to one affine map h -> A h + B per channel, and the maps
-// are folded in token order: over the warps through shared memory, over the cluster's tiles
-// through distributed shared memory.  Every CTA folds the same maps in the same order, so results
-// do not depend on timing, and the carry never goes through global memory.
+// An element is 6 to 16 bytes and some 35 (forward) to 75 (backward) instructions, so neither HBM nor the
+// issue slots have room to spare, and a scan that read its inputs twice would lose to HBM at once.  It
+// needs no second reading when whoever reads a tile also finishes it: a cluster of CTAs walks along one
+// (sequence, head), each CTA taking every cluster-size-th tile of 64 tokens x d channels.  Inside the CTA
+// a warp holds consecutive tokens (a lane: four channels) and reduces them to one affine map
+// h -> A h + B per channel; the maps are folded in token order, over the warps through shared memory,
+// over the cluster's tiles through distributed shared memory.  Every CTA folds the same maps in the
+// same order, so results do not depend on timing, and the carry never goes through global memory.
+//
+// Measured (B200, H = 32, d = 128): forward, 131072 tokens in bf16 with the normalised input, 0.905 ms for
+// 3.24 GB (3.6 TB/s, 55 % of the copy rate): 128 of the 148 SMs work (32 heads x 4 CTAs), at 77 % of their
+// issue slots.  32768 packed tokens with fp32 gates: forward 0.250 ms (1.07 GB), backward 0.575 ms (1.88 GB,
+// 50 %), where 16 warps in step leave issue slots empty behind waits and shared-memory latency.
 //
 // The backward pass walks the tiles in reverse.  The forward pass has kept the state entering each
 // tile (1/64 of the fp32 size of the outputs), so h_{t-1} is rebuilt inside the tile and only D is

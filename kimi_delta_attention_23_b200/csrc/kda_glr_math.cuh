@@ -1,11 +1,11 @@
 // kda_glr_math.cuh -- the gate of the gated linear recurrence in packed two-lane fp32 arithmetic.
 //
-// The forward pass at HBM speed has about 13 issue slots and 6 MUFU cycles per element and SM
-// sub-core to spend, so the gate is evaluated two channels at a time (fma.rn.f32x2 and friends)
-// with two MUFU operations per element: e = 2^(-|z| log2 e) and a = 2^(g log2 e) (a polynomial where a is near 1).  softplus(z) =
-// max(z, 0) + log1p(e) takes log1p as e times a degree-7 polynomial: a logarithm of the rounded
-// 1 + e would lose the gates of slow channels (softplus << 1), whose decays multiply up over
-// thousands of tokens.
+// The forward pass at HBM speed has about 13 issue slots per element and SM sub-core, so the gate is
+// evaluated two channels at a time (fma.rn.f32x2 and friends), with two MUFU operations per element:
+// e = 2^(-|z| log2 e) and a = 2^(g log2 e).  softplus(z) = max(z, 0) + log1p(e) takes log1p as e times a
+// degree-7 polynomial: a logarithm of the rounded 1 + e would lose the gates of slow channels
+// (softplus << 1), whose decays multiply up over thousands of tokens; decays near 1 come from a
+// polynomial for the same reason.
 //
 // Both polynomials are weighted least-squares fits on Chebyshev nodes made for this file, with the
 // largest relative error of their fp32 Horner evaluation beside them.

@@ -14,7 +14,12 @@ constexpr int32_t kMaxNodes = 64;
 constexpr int32_t kMaxCopies = 8192;  // pairs of one simultaneous copy: 16 bytes of each fit shared memory
 
 bool dtype_ok(kda_dtype_t t) { return t == KDA_F32 || t == KDA_BF16; }
-kda_status_t done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+// a failed launch is told by the status alone: the runtime's record of it would be found by whoever asks next
+kda_status_t done(cudaError_t e) {
+  if (e == cudaSuccess) return KDA_OK;
+  cudaGetLastError();
+  return KDA_ERR_CUDA;
+}
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 bool work_ok(const void* p, size_t have, size_t need) {
   return need == 0 || (p && have >= need && !(reinterpret_cast<uintptr_t>(p) & 255u));
