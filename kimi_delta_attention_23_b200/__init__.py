@@ -23,8 +23,8 @@ Public calls (same names as the C ABI):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -203,8 +203,25 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-# The calls that serve single tokens take a few microseconds on the device, so their wrappers check
-# each tensor in one go and leave it to the functions above to say what is wrong.
+# The calls that serve single tokens take a few microseconds on the device, so their wrappers have all
+# tensors checked in one go (_check.so, built beside libkda.so); only where something is not as it
+# should be do the functions here look closer and say what it is.
+def _checker(expectations):
+    """A function of the tensors: device number, extents, addresses and types for the C ABI, or None."""
+    made = []
+
+    def look(*tensors):
+        if not made:
+            try:
+                from . import _check
+            except ImportError as e:
+                raise ImportError("_check.so is not built; run kimi_delta_attention_23_b200/build.py") from e
+            made.append(functools.partial(_check.check, _check.make(expectations)))
+        return made[0](*tensors)
+
+    return look
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -250,12 +267,12 @@ def _on_stream(stream, index):
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _on_device(index):
-    """Makes device ``index`` the current one for a launch, at no cost where it already is."""
-    return _HERE_ALREADY if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-
-_HERE_ALREADY = contextlib.nullcontext()
+def _launch(index, call, *args):
+    """A call of the C ABI with device ``index`` current."""
+    if index == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
 
 
 def _used_on(stream, index, *tensors):

@@ -1,4 +1,5 @@
-"""Build libkda.so in-tree: every csrc/*.cu compiled for sm_100a and linked into one library."""
+"""Build in-tree: libkda.so, every csrc/*.cu compiled for sm_100a and linked into one library, and _check.so,
+the binding's checks of a call's tensors (csrc/kda_check.cpp, compiled against this Python and torch)."""
 import concurrent.futures as cf
 import glob
 import os
@@ -9,6 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkda.so")
+CHECK_SRC = os.path.join(CSRC, "kda_check.cpp")
+CHECK_LIB = os.path.join(HERE, "_check.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -42,7 +45,30 @@ def _compile(src, verbose):
     return obj, r.stderr
 
 
+def build_check(force=False):
+    """_check.so, if it is missing or older than its source."""
+    if not force and os.path.exists(CHECK_LIB) and os.path.getmtime(CHECK_LIB) >= os.path.getmtime(CHECK_SRC):
+        return CHECK_LIB
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    tmp = CHECK_LIB + ".tmp"
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                        "-isystem", os.path.join(root, "include"),
+                        "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                        "-isystem", sysconfig.get_paths()["include"], CHECK_SRC, "-o", tmp, "-L" + lib,
+                        "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CHECK_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CHECK_LIB)
+    return CHECK_LIB
+
+
 def build(force=False, verbose=False):
+    build_check(force)
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

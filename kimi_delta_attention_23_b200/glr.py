@@ -19,7 +19,8 @@ import ctypes
 
 import torch
 
-from . import (_DTYPES, KdaError, _dev, _flags, _need, _need_rank, _on_device, _on_stream, _used_on, _where, load_library)
+from . import (_checker, _DTYPES, KdaError, _dev, _flags, _launch, _need, _need_rank, _on_stream, _used_on, _where,
+               load_library)
 
 __all__ = ["kda_glr_fwd", "kda_glr_bwd", "kda_glr_decode", "kda_glr_checkpoint_shape", "kda_glr_bwd_workspace_size"]
 
@@ -49,6 +50,9 @@ def kda_glr_bwd_workspace_size(total_tokens, batch, num_heads, d) -> int:
     return int(load_library().kda_glr_bwd_workspace_size(total_tokens, batch, num_heads, d))
 
 
+_CELLS = "x v T,H,d; raw g T,H,d; beta f T,H; a_log f H; dt_bias f H,d"
+_FWD = _checker(_CELLS + "; cu i B+1; pool f S,H,d; idx i B")
+_DECODE = _checker(_CELLS + "; pool f S,H,d; idx i T")
 _FLAGS = {}
 
 
@@ -116,20 +120,22 @@ def kda_glr_fwd(x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool
     [T,H,d] in ``output_dtype`` (default: the dtype of x); rows outside every sequence are not written.
     ``checkpoints`` (f32, kda_glr_checkpoint_shape(T, B, H, d)) keeps what kda_glr_bwd needs.
     """
-    lib = load_library()
-    index, T, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
-    B, cu = _offsets(cu_seqlens, x, index)
-    pool, slots, indices = _pool(state_pool, state_indices, x, index, B, H, d)
+    lib, flags = load_library(), _glr_flags(gate_mode, beta_mode, input_mode)
+    found = _FWD(x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices)
+    if found is None:
+        index, T, H, d, (xs, x_type, raws, gate_type, betas, a_logs, biases) = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+        B, cu = _offsets(cu_seqlens, x, index)
+        pool, slots, indices = _pool(state_pool, state_indices, x, index, B, H, d)
+    else:
+        index, T, H, d, B, slots, xs, raws, betas, a_logs, biases, cu, pool, indices, x_type, gate_type = found
     kept = None
     if checkpoints is not None:
         kept = _need(checkpoints, "checkpoints", torch.float32, (lib.kda_glr_checkpoints(T, B), H, d), x, index)
-    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, x, index)
-    given = out
+    status, given = _status(device_status, x, index), out
     out, to, out_type = _output(out, output_dtype, x, index)
-    with _on_device(index):
-        rc = lib.kda_glr_fwd(*inputs, cu, B, T, H, d, pool, slots, indices, to, out_type, kept, flags, gate_lower_bound,
-                             status, _on_stream(stream, index))
-    if given is None:
+    rc = _launch(index, lib.kda_glr_fwd, xs, x_type, raws, gate_type, betas, a_logs, biases, cu, B, T, H, d, pool, slots,
+                 indices, to, out_type, kept, flags, gate_lower_bound, status, _on_stream(stream, index))
+    if given is None and stream is not None:
         _used_on(stream, index, out)
     if rc != 0:
         raise KdaError(rc, "kda_glr_fwd")
@@ -140,16 +146,18 @@ def kda_glr_decode(x, raw_gate, beta_logits, a_log, dt_bias, state_pool, state_i
                    gate_mode="original", beta_mode="logits", input_mode="unit", gate_lower_bound=-5.0,
                    device_status=None, stream=None):
     """One token of each sequence: x, raw_gate [B,H,d]; beta_logits [B,H]; the rest as kda_glr_fwd."""
-    lib = load_library()
-    index, B, H, d, inputs = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
-    pool, slots, indices = _pool(state_pool, state_indices, x, index, B, H, d)
-    flags, status = _glr_flags(gate_mode, beta_mode, input_mode), _status(device_status, x, index)
-    given = out
+    lib, flags = load_library(), _glr_flags(gate_mode, beta_mode, input_mode)
+    found = _DECODE(x, raw_gate, beta_logits, a_log, dt_bias, state_pool, state_indices)
+    if found is None:
+        index, B, H, d, (xs, x_type, raws, gate_type, betas, a_logs, biases) = _inputs(x, raw_gate, beta_logits, a_log, dt_bias)
+        pool, slots, indices = _pool(state_pool, state_indices, x, index, B, H, d)
+    else:
+        index, B, H, d, slots, xs, raws, betas, a_logs, biases, pool, indices, x_type, gate_type = found
+    status, given = _status(device_status, x, index), out
     out, to, out_type = _output(out, output_dtype, x, index)
-    with _on_device(index):
-        rc = lib.kda_glr_decode(*inputs, B, H, d, pool, slots, indices, to, out_type, flags, gate_lower_bound, status,
-                                _on_stream(stream, index))
-    if given is None:
+    rc = _launch(index, lib.kda_glr_decode, xs, x_type, raws, gate_type, betas, a_logs, biases, B, H, d, pool, slots, indices,
+                 to, out_type, flags, gate_lower_bound, status, _on_stream(stream, index))
+    if given is None and stream is not None:
         _used_on(stream, index, out)
     if rc != 0:
         raise KdaError(rc, "kda_glr_decode")
@@ -196,14 +204,14 @@ def kda_glr_bwd(dout, x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, chec
     da_log, das = grad(da_log, "da_log", (H,))
     ddt_bias, dbs = grad(ddt_bias, "ddt_bias", (H, d))
     d_initial, dis = grad(d_initial, "d_initial", (B, H, d))
-    with _on_device(index):
-        if workspace is None:
-            workspace = torch.empty(lib.kda_glr_bwd_workspace_size(T, B, H, d), dtype=torch.uint8, device=x.device)
-            made.append(workspace)
-        _dev(workspace, "workspace", torch.uint8, x.device)
-        rc = lib.kda_glr_bwd(douts, _DTYPES[dtype], *inputs, cu, B, T, H, d, kept, final, dxs, draws, dbetas, das, dbs, dis,
-                             flags, gate_lower_bound, workspace.data_ptr(), workspace.numel(), status,
-                             _on_stream(stream, index))
+    if workspace is None:
+        need = _launch(index, lib.kda_glr_bwd_workspace_size, T, B, H, d)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        made.append(workspace)
+    _dev(workspace, "workspace", torch.uint8, x.device)
+    rc = _launch(index, lib.kda_glr_bwd, douts, _DTYPES[dtype], *inputs, cu, B, T, H, d, kept, final, dxs, draws, dbetas, das,
+                 dbs, dis, flags, gate_lower_bound, workspace.data_ptr(), workspace.numel(), status,
+                 _on_stream(stream, index))
     _used_on(stream, index, *made)
     if rc != 0:
         raise KdaError(rc, "kda_glr_bwd")

@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import KdaError, _dev, _need, _need_rank, _on_device, _on_stream, _used_on, load_library
+from . import KdaError, _dev, _launch, _need, _need_rank, _on_stream, _used_on, load_library
 
 __all__ = ["kda_pool_copy", "kda_pool_fork", "kda_pool_free", "kda_pool_compact", "kda_pool_workspace_size",
            "MAX_POOL_COPIES"]
@@ -58,19 +58,16 @@ def _call(what, pool, layout, lists, n, results, workspace, device_status, strea
     _, index, layers, slots, elems = layout
     lib = load_library()
     status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), pool, index)
-    with _on_device(index):
-        if workspace is None and what == "kda_pool_copy" and n <= FEW_COPIES:
-            at, size = None, 0
-        elif workspace is None:
-            workspace = torch.empty(lib.kda_pool_workspace_size(n, slots), dtype=torch.uint8, device=pool.device)
-            made = (*made, workspace)
-            at, size = workspace.data_ptr(), workspace.numel()
-        else:
-            _dev(workspace, "workspace", torch.uint8, pool.device)
-            at, size = workspace.data_ptr(), workspace.numel()
-        rc = getattr(lib, what)(pool.data_ptr(), layers, slots, elems, *lists, n, *results, at, size, status,
-                                _on_stream(stream, index))
-    _used_on(stream, index, *made)
+    if workspace is not None:
+        _dev(workspace, "workspace", torch.uint8, pool.device)
+    elif what != "kda_pool_copy" or n > FEW_COPIES:
+        workspace = torch.empty(lib.kda_pool_workspace_size(n, slots), dtype=torch.uint8, device=pool.device)
+        made = (*made, workspace)
+    at, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    rc = _launch(index, getattr(lib, what), pool.data_ptr(), layers, slots, elems, *lists, n, *results, at, size, status,
+                 _on_stream(stream, index))
+    if stream is not None:
+        _used_on(stream, index, *made)
     if rc != 0:
         raise KdaError(rc, what)
 

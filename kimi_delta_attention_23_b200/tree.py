@@ -11,7 +11,8 @@ import ctypes
 
 import torch
 
-from . import _DTYPES, KdaError, _flags, _need, _need_rank, _on_device, _on_stream, _used_on, _where, load_library
+from . import (_checker, _DTYPES, KdaError, _flags, _launch, _need, _need_rank, _on_stream, _used_on, _where,
+               load_library)
 
 __all__ = ["kda_tree_decode", "kda_tree_commit", "MAX_TREE_NODES"]
 
@@ -27,6 +28,11 @@ SIGNATURES = {
 }
 
 
+_BLOCKS = {"K_FIRST": "S,Hv,dk,dv", "V_FIRST": "S,Hv,dv,dk"}
+_TREE = {layout: _checker("q v M,Hk,dk; k s M,Hk,dk; v s M,Hv,dv; raw f M,Hv,dk; beta f M,Hv; a_log f Hv; dt_bias f Hv,dk; "
+                          f"cu i B+1; parents i M; pool f {block}; idx i B") for layout, block in _BLOCKS.items()}
+_COMMIT = {layout: _checker("k v M,Hk,dk; deltas f M,Hv,dv; raw f M,Hv,dk; a_log f Hv; dt_bias f Hv,dk; cu i B+1; parents i M; "
+                            f"accepted i B; pool f {block}; idx i B") for layout, block in _BLOCKS.items()}
 _FLAGS = {}
 
 
@@ -37,15 +43,19 @@ def _tree_flags(gate_mode, beta_mode, state_layout):
     return _FLAGS[key]
 
 
-def _tree(cu_nodes, parents, max_nodes, M, like, index):
+def _tree(cu_nodes, parents, M, like, index):
     (count,), cu = _need_rank(cu_nodes, "cu_nodes", torch.int32, 1, like, index)
     if count < 1:
         raise ValueError("cu_nodes must hold B + 1 offsets")
+    return count - 1, cu, _need(parents, "parents", torch.int32, (M,), like, index)
+
+
+def _most(max_nodes, M):
     if max_nodes is None:
-        max_nodes = max(1, min(M, MAX_TREE_NODES))
+        return max(1, min(M, MAX_TREE_NODES))
     if not 1 <= max_nodes <= MAX_TREE_NODES:
         raise ValueError(f"max_nodes must be 1 .. {MAX_TREE_NODES}, got {max_nodes}")
-    return count - 1, int(max_nodes), cu, _need(parents, "parents", torch.int32, (M,), like, index)
+    return int(max_nodes)
 
 
 def _pool(state_pool, state_indices, state_layout, like, index, B, Hv, dk, dv):
@@ -69,41 +79,44 @@ def kda_tree_decode(q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_nodes, pa
     M, at most 64); naming it close to the real size takes a smaller kernel.  Returns (out [M,Hv,dv],
     deltas [M,Hv,dv] f32), the second for kda_tree_commit.
     """
-    lib = load_library()
-    index, (M, Hk, dk), qs = _where(q, "q", 3)
-    dtype = q.dtype
-    if dtype not in _DTYPES:
-        raise ValueError("q/k/v must be float32 or bfloat16")
-    ks = _need(k, "k", dtype, (M, Hk, dk), q, index)
-    (rows, Hv, dv), vs = _need_rank(v, "v", dtype, 3, q, index)
-    if rows != M:
-        raise ValueError(f"v has shape {tuple(v.shape)}, expected [{M}, Hv, dv]")
-    raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), q, index)
-    betas = _need(beta_logits, "beta_logits", torch.float32, (M, Hv), q, index)
-    alogs = _need(a_log, "a_log", torch.float32, (Hv,), q, index)
-    biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), q, index)
-    B, max_nodes, cu, pars = _tree(cu_nodes, parents, max_nodes, M, q, index)
-    flags = _tree_flags(gate_mode, beta_mode, state_layout)
-    pool, slots, indices = _pool(state_pool, state_indices, state_layout, q, index, B, Hv, dk, dv)
+    lib, flags = load_library(), _tree_flags(gate_mode, beta_mode, state_layout)
+    found = _TREE[state_layout](q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_nodes, parents, state_pool, state_indices)
+    if found is None:
+        index, (M, Hk, dk), qs = _where(q, "q", 3)
+        dtype = q.dtype
+        if dtype not in _DTYPES:
+            raise ValueError("q/k/v must be float32 or bfloat16")
+        ks = _need(k, "k", dtype, (M, Hk, dk), q, index)
+        (rows, Hv, dv), vs = _need_rank(v, "v", dtype, 3, q, index)
+        if rows != M:
+            raise ValueError(f"v has shape {tuple(v.shape)}, expected [{M}, Hv, dv]")
+        raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), q, index)
+        betas = _need(beta_logits, "beta_logits", torch.float32, (M, Hv), q, index)
+        alogs = _need(a_log, "a_log", torch.float32, (Hv,), q, index)
+        biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), q, index)
+        B, cu, pars = _tree(cu_nodes, parents, M, q, index)
+        pool, slots, indices = _pool(state_pool, state_indices, state_layout, q, index, B, Hv, dk, dv)
+        in_type = _DTYPES[dtype]
+    else:
+        index, M, Hk, dk, Hv, dv, B, slots, qs, ks, vs, raws, betas, alogs, biases, cu, pars, pool, indices, in_type = found
+    max_nodes = _most(max_nodes, M)
     if output_dtype is None:
         output_dtype = v.dtype if out is None else out.dtype
     if output_dtype not in _DTYPES:
         raise ValueError("output_dtype must be float32 or bfloat16")
     status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), q, index)
-    made = []
-    if out is None:
+    new_out, new_deltas = out is None, deltas is None
+    if new_out:
         out = torch.empty_like(v, dtype=output_dtype)
-        made.append(out)
-    if deltas is None:
+    if new_deltas:
         deltas = torch.empty_like(v, dtype=torch.float32)
-        made.append(deltas)
-    with _on_device(index):
-        rc = lib.kda_tree_decode(qs, ks, vs, _DTYPES[dtype], raws, betas, alogs, biases, cu, pars, B, M,
-                                 max_nodes, Hk, Hv, dk, dv, pool, slots, indices,
-                                 _need(out, "out", output_dtype, (M, Hv, dv), q, index), _DTYPES[output_dtype],
-                                 _need(deltas, "deltas", torch.float32, (M, Hv, dv), q, index), flags,
-                                 gate_lower_bound, status, _on_stream(stream, index))
-    _used_on(stream, index, *made)
+    rc = _launch(index, lib.kda_tree_decode, qs, ks, vs, in_type, raws, betas, alogs, biases, cu, pars, B, M, max_nodes, Hk,
+                 Hv, dk, dv, pool, slots, indices,
+                 out.data_ptr() if new_out else _need(out, "out", output_dtype, (M, Hv, dv), q, index), _DTYPES[output_dtype],
+                 deltas.data_ptr() if new_deltas else _need(deltas, "deltas", torch.float32, (M, Hv, dv), q, index), flags,
+                 gate_lower_bound, status, _on_stream(stream, index))
+    if stream is not None:
+        _used_on(stream, index, out if new_out else None, deltas if new_deltas else None)
     if rc != 0:
         raise KdaError(rc, "kda_tree_decode")
     return out, deltas
@@ -117,24 +130,27 @@ def kda_tree_commit(k, raw_gate, a_log, dt_bias, deltas, cu_nodes, parents, acce
     ``accepted`` [B] i32: the last accepted node of each sequence, numbered within it (-1: none, the
     state stays).  The other tensors as in the kda_tree_decode call that returned ``deltas``.
     """
-    lib = load_library()
-    index, (M, Hk, dk), ks = _where(k, "k", 3)
-    if k.dtype not in _DTYPES:
-        raise ValueError("k must be float32 or bfloat16")
-    (rows, Hv, dv), found = _need_rank(deltas, "deltas", torch.float32, 3, k, index)
-    if rows != M:
-        raise ValueError(f"deltas has shape {tuple(deltas.shape)}, expected [{M}, Hv, dv]")
-    raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), k, index)
-    alogs = _need(a_log, "a_log", torch.float32, (Hv,), k, index)
-    biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), k, index)
-    B, max_nodes, cu, pars = _tree(cu_nodes, parents, max_nodes, M, k, index)
-    took = _need(accepted, "accepted", torch.int32, (B,), k, index)
-    flags = _tree_flags(gate_mode, "logits", state_layout)
-    pool, slots, indices = _pool(state_pool, state_indices, state_layout, k, index, B, Hv, dk, dv)
+    lib, flags = load_library(), _tree_flags(gate_mode, "logits", state_layout)
+    found = _COMMIT[state_layout](k, deltas, raw_gate, a_log, dt_bias, cu_nodes, parents, accepted, state_pool, state_indices)
+    if found is None:
+        index, (M, Hk, dk), ks = _where(k, "k", 3)
+        if k.dtype not in _DTYPES:
+            raise ValueError("k must be float32 or bfloat16")
+        (rows, Hv, dv), dls = _need_rank(deltas, "deltas", torch.float32, 3, k, index)
+        if rows != M:
+            raise ValueError(f"deltas has shape {tuple(deltas.shape)}, expected [{M}, Hv, dv]")
+        raws = _need(raw_gate, "raw_gate", torch.float32, (M, Hv, dk), k, index)
+        alogs = _need(a_log, "a_log", torch.float32, (Hv,), k, index)
+        biases = _need(dt_bias, "dt_bias", torch.float32, (Hv, dk), k, index)
+        B, cu, pars = _tree(cu_nodes, parents, M, k, index)
+        took = _need(accepted, "accepted", torch.int32, (B,), k, index)
+        pool, slots, indices = _pool(state_pool, state_indices, state_layout, k, index, B, Hv, dk, dv)
+        k_type = _DTYPES[k.dtype]
+    else:
+        index, M, Hk, dk, Hv, dv, B, slots, ks, dls, raws, alogs, biases, cu, pars, took, pool, indices, k_type = found
+    max_nodes = _most(max_nodes, M)
     status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), k, index)
-    with _on_device(index):
-        rc = lib.kda_tree_commit(ks, _DTYPES[k.dtype], raws, alogs, biases, found, cu, pars, took, B, M,
-                                 max_nodes, Hk, Hv, dk, dv, pool, slots, indices, flags, gate_lower_bound, status,
-                                 _on_stream(stream, index))
+    rc = _launch(index, lib.kda_tree_commit, ks, k_type, raws, alogs, biases, dls, cu, pars, took, B, M, max_nodes, Hk, Hv,
+                 dk, dv, pool, slots, indices, flags, gate_lower_bound, status, _on_stream(stream, index))
     if rc != 0:
         raise KdaError(rc, "kda_tree_commit")
