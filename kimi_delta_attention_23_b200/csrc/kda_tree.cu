@@ -21,14 +21,14 @@
 //  3. blocks of 16 nodes down the tree: a product with the deltas of the blocks before, then a thread per
 //     value column substitutes within the block; a last product gives the outputs.
 // The state's 4 dk dv bytes are the floor (64 requests x 16 nodes x 32 heads: 26 us; 32 x 64 nodes: 27 us).
-// Measured 57 and 152 us: a small tree is a chain of short phases, and four CTAs per SM are what the
+// Measured 58 and 153 us: a small tree is a chain of short phases, and four CTAs per SM are what the
 // registers allow to overlap; a 64-node tree spends 20 % on the product with S (mma.sync at 8 cycles per
 // instruction and sub-core, its limit), a third on the walks and the loads before it, and a third on the
 // four blocks of the solve.  tcgen05 would take the first of these: with 2 N <= 128 rows against a state that
 // is read once it would also need S split and staged in shared memory in its layout, about what it saves.
 //
 // The commit is S' = e^{G_a} o S + sum over the path (k_j o e^{G_a - G_j}) u_j^T, one pass over the
-// state, bound by its 8 dk dv bytes: 45 us for 64 states of 32 heads, 94 % of the copy rate.
+// state, bound by its 8 dk dv bytes: 49 us for 64 states of 32 heads, 87 % of the copy rate.
 #include <type_traits>
 
 #include "kda_glr_math.cuh"
