@@ -20,7 +20,7 @@
 // same order, so results do not depend on timing, and the carry never goes through global memory.
 //
 // Measured (B200, H = 32, d = 128): forward, 131072 tokens in bf16 with the normalised input, 0.905 ms for
-// 3.24 GB (3.6 TB/s, 55 % of the copy rate): 128 of the 148 SMs work (32 heads x 4 CTAs), at 77 % of their
+// 3.24 GB (3.6 TB/s, 55 % of the copy rate): 128 of the 148 SMs work (32 heads x 4 CTAs), at 68 % of their
 // issue slots.  32768 packed tokens with fp32 gates: forward 0.250 ms (1.07 GB), backward 0.575 ms (1.88 GB,
 // 50 %), where 16 warps in step leave issue slots empty behind waits and shared-memory latency.
 //

@@ -21,14 +21,14 @@
 //  3. blocks of 16 nodes down the tree: a product with the deltas of the blocks before, then a thread per
 //     value column substitutes within the block; a last product gives the outputs.
 // The state's 4 dk dv bytes are the floor (64 requests x 16 nodes x 32 heads: 26 us; 32 x 64 nodes: 27 us).
-// Measured 58 and 153 us: a small tree is a chain of short phases, and four CTAs per SM are what the
+// Measured 55 and 153 us: a small tree is a chain of short phases, and four CTAs per SM are what the
 // registers allow to overlap; a 64-node tree spends 20 % on the product with S (mma.sync at 8 cycles per
 // instruction and sub-core, its limit), a third on the walks and the loads before it, and a third on the
 // four blocks of the solve.  tcgen05 would take the first of these: with 2 N <= 128 rows against a state that
 // is read once it would also need S split and staged in shared memory in its layout, about what it saves.
 //
 // The commit is S' = e^{G_a} o S + sum over the path (k_j o e^{G_a - G_j}) u_j^T, one pass over the
-// state, bound by its 8 dk dv bytes: 49 us for 64 states of 32 heads, 87 % of the copy rate.
+// state, bound by its 8 dk dv bytes: 48 us for 64 states of 32 heads, 89 % of the copy rate.
 #include <type_traits>
 
 #include "kda_glr_math.cuh"
@@ -380,65 +380,105 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
     }
   };
   if constexpr (kNodes == 64) load_values(0);  // where the registers allow it, ahead of the products
-#pragma unroll 1
-  for (int group = warp; group < 8; group += kWarps) {
-    const int col = 16 * group + 2 * gr;  // a lane's first column of S
+  // a lane's elements of the state: channels 16 ks + 4 q .. + 3 of columns 16 group + 2 gr and the next
+  auto load_state = [&](int group, int ks, float (&s)[2][4]) {
+    const int c = 16 * ks + 4 * q, col = 16 * group + 2 * gr;
+    if constexpr (kFull && kVFirst) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const float4 v = *reinterpret_cast<const float4*>(from + (col + t) * 128 + c);
+        s[t][0] = v.x, s[t][1] = v.y, s[t][2] = v.z, s[t][3] = v.w;
+      }
+    } else if constexpr (kFull) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = *reinterpret_cast<const float2*>(from + (c + e) * 128 + col);
+        s[0][e] = v.x, s[1][e] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[t][e] = c + e < dk && col + t < dv ? state[state_off(c + e, col + t, dk, dv, kVFirst)] : 0.f;
+    }
+  };
+  auto load_factors = [&](int tile, int ks, Left<kExact>& left) {
+    const int c = 16 * ks + 4 * q, r = 16 * tile + gr;
+    if constexpr (kExact) {
+      left.set(*reinterpret_cast<const float4*>(&sm.factor[r][c]), *reinterpret_cast<const float4*>(&sm.factor[r + 8][c]));
+    } else {
+      const uint2 h0 = *reinterpret_cast<const uint2*>(&sm.hi[r][c]), h1 = *reinterpret_cast<const uint2*>(&sm.hi[r + 8][c]);
+      const uint2 l0 = *reinterpret_cast<const uint2*>(&sm.lo[r][c]), l1 = *reinterpret_cast<const uint2*>(&sm.lo[r + 8][c]);
+      left.hi[0] = h0.x, left.hi[1] = h1.x, left.hi[2] = h0.y, left.hi[3] = h1.y;
+      left.lo[0] = l0.x, left.lo[1] = l1.x, left.lo[2] = l0.y, left.lo[3] = l1.y;
+    }
+  };
+  // accumulator n = 2 (lane % 4) + {0, 1} of n-tile nt is column 16 group + 2 n + nt
+  auto put = [&](int tile, int group, const float (&big)[2][4], const float (&small)[2][4]) {
+    const int at = 16 * group + 4 * q, i = 8 * tile + gr;
+    *reinterpret_cast<float4*>(&sm.u[i][at]) =
+        make_float4(big[0][0] + small[0][0], big[1][0] + small[1][0], big[0][1] + small[0][1], big[1][1] + small[1][1]);
+    *reinterpret_cast<float4*>(&sm.qs[i][at]) =
+        make_float4(big[0][2] + small[0][2], big[1][2] + small[1][2], big[0][3] + small[0][3], big[1][3] + small[1][3]);
+  };
+  if constexpr (kStaged<kNodes>) {
+    static_assert(kCols == 1, "a warp takes one group");
     Right<kExact> right[8][2];  // [k-step][n-tile]
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
-      const int c = 16 * ks + 4 * q;
       float s[2][4];
-      if constexpr (kFull && kVFirst) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float4 v = *reinterpret_cast<const float4*>(from + (col + t) * 128 + c);
-          s[t][0] = v.x, s[t][1] = v.y, s[t][2] = v.z, s[t][3] = v.w;
-        }
-      } else if constexpr (kFull) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = *reinterpret_cast<const float2*>(from + (c + e) * 128 + col);
-          s[0][e] = v.x, s[1][e] = v.y;
-        }
-      } else {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[t][e] = c + e < dk && col + t < dv ? state[state_off(c + e, col + t, dk, dv, kVFirst)] : 0.f;
-      }
+      load_state(warp, ks, s);
 #pragma unroll
       for (int t = 0; t < 2; ++t) right[ks][t].set(s[t][0], s[t][1], s[t][2], s[t][3]);
     }
-    if (group == warp) __syncthreads();  // the factors are there, and a staged state has been read: u and qs take its place
+    __syncthreads();  // the factors are there, and the state has been read: u and qs take its place
     const int tiles = (n + 7) >> 3;
     for (int t = 0; t < tiles; ++t) {
       float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const int c = 16 * ks + 4 * q;
         Left<kExact> left;
-        if constexpr (kExact) {
-          left.set(*reinterpret_cast<const float4*>(&sm.factor[16 * t + gr][c]),
-                   *reinterpret_cast<const float4*>(&sm.factor[16 * t + gr + 8][c]));
-        } else {
-          const uint2 h0 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + gr][c]);
-          const uint2 h1 = *reinterpret_cast<const uint2*>(&sm.hi[16 * t + gr + 8][c]);
-          const uint2 l0 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + gr][c]);
-          const uint2 l1 = *reinterpret_cast<const uint2*>(&sm.lo[16 * t + gr + 8][c]);
-          left.hi[0] = h0.x, left.hi[1] = h1.x, left.hi[2] = h0.y, left.hi[3] = h1.y;
-          left.lo[0] = l0.x, left.lo[1] = l1.x, left.lo[2] = l0.y, left.lo[3] = l1.y;
-        }
+        load_factors(t, ks, left);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) multiply<kExact>(big[nt], small[nt], left, right[ks][nt]);
       }
-      // accumulator n = 2 (lane % 4) + {0, 1} of tile nt is column 16 warp + 2 n + nt
-      const int c0 = 16 * group + 4 * q, i = 8 * t + gr;
-      *reinterpret_cast<float4*>(&sm.u[i][c0]) =
-          make_float4(big[0][0] + small[0][0], big[1][0] + small[1][0], big[0][1] + small[0][1], big[1][1] + small[1][1]);
-      *reinterpret_cast<float4*>(&sm.qs[i][c0]) =
-          make_float4(big[0][2] + small[0][2], big[1][2] + small[1][2], big[0][3] + small[0][3], big[1][3] + small[1][3]);
+      put(t, warp, big, small);
     }
+  } else {
+    // few rows: all of them are accumulated while the state streams by, a k-step ahead (1: 54.3 us at 64
+    // sequences of up to 16 nodes and 32 heads, 2: 55.1, 3: 55.8, 4: 60.2; one group of columns after the other: 58)
+    constexpr int kTiles = kNodes / 8, kAhead = 1;
+    float s[kAhead + 1][kCols][2][4], big[kTiles][kCols][2][4] = {}, small[kTiles][kCols][2][4] = {};
+#pragma unroll
+    for (int ks = 0; ks < kAhead; ++ks)
+#pragma unroll
+      for (int g = 0; g < kCols; ++g) load_state(warp + kWarps * g, ks, s[ks][g]);
+    __syncthreads();  // the factors are there
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      if (ks + kAhead < 8) {
+#pragma unroll
+        for (int g = 0; g < kCols; ++g) load_state(warp + kWarps * g, ks + kAhead, s[(ks + kAhead) % (kAhead + 1)][g]);
+      }
+      Left<kExact> left[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) load_factors(t, ks, left[t]);
+#pragma unroll
+      for (int g = 0; g < kCols; ++g)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float(&w)[4] = s[ks % (kAhead + 1)][g][nt];
+          Right<kExact> right;
+          right.set(w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) multiply<kExact>(big[t][g][nt], small[t][g][nt], left[t], right);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int g = 0; g < kCols; ++g) put(t, warp + kWarps * g, big[t][g], small[t][g]);
   }
   __syncthreads();
 
