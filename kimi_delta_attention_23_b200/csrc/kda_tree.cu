@@ -14,23 +14,18 @@
 //     to the node is a running product of the tokens' decays (never an exponential of a sum, so
 //     nothing over- or underflows early), which at the root is e^{G_i} itself.
 //  2. P = [K o e^G; Q o e^G] S on mma.sync, S in the B fragments.  kda_tree_commit writes what comes of
-//     this into fp32 states, which single bf16 or tf32 products would spoil, so every fp32 factor is split
-//     into two parts and three of the four partial products are summed.  From fp32 inputs, or where fp32
-//     outputs are asked for, the parts are tf32: 2^-21 of the factors is lost.  Between bf16 inputs and bf16
-//     outputs they are bf16, in half the products: 2^-17 is lost, next to the 2^-9 that v itself has lost.
+//     this into fp32 states, and a good prediction k^T S all but cancels v, so the products must be as good
+//     as fp32's whatever the types of the inputs and outputs: every factor is split into two tf32 parts
+//     (at most 2^-22 of it is lost) and three of the four partial products are summed.
 //  3. blocks of 16 nodes down the tree: a product with the deltas of the blocks before, then a thread per
 //     value column substitutes within the block; a last product gives the outputs.
 // The state's 4 dk dv bytes are the floor (64 requests x 16 nodes x 32 heads: 26 us; 32 x 64 nodes: 27 us).
-// Measured 55 and 153 us: a small tree is a chain of short phases, and four CTAs per SM are what the
-// registers allow to overlap; a 64-node tree spends 20 % on the product with S (mma.sync at 8 cycles per
-// instruction and sub-core, its limit), a third on the walks and the loads before it, and a third on the
-// four blocks of the solve.  tcgen05 would take the first of these: with 2 N <= 128 rows against a state that
-// is read once it would also need S split and staged in shared memory in its layout, about what it saves.
+// Measured 59 and 197 us: a small tree is a chain of short phases, and four CTAs per SM are what the
+// registers allow to overlap; a 64-node tree runs as one CTA per SM, whose phases follow one another, and
+// its products take 6 mma.sync of tf32 where unsplit ones would take 2.
 //
 // The commit is S' = e^{G_a} o S + sum over the path (k_j o e^{G_a - G_j}) u_j^T, one pass over the
 // state, bound by its 8 dk dv bytes: 48 us for 64 states of 32 heads, 89 % of the copy rate.
-#include <type_traits>
-
 #include "kda_glr_math.cuh"
 #include "kda_ops_internal.h"
 #include "kda_sm100.cuh"
@@ -41,7 +36,7 @@ namespace {
 constexpr int kThreads = 256;     // of the commit
 constexpr int kPitch = 132;    // floats of a node's row in shared memory
 constexpr uint64_t kWaitNs = 1000000000ull;  // limit of the wait for a copy
-constexpr int kPitchH = 144;   // elements of a factor's row: 32 (bf16) or 64 (fp32) bytes past a whole line
+constexpr int kPitchH = 144;   // floats of a factor's row: 64 bytes past a whole line
 
 // Offsets and slot of a sequence; false where one is out of range.
 __device__ __forceinline__ bool tree_at(const TreeArgs& a, int b, int32_t& m0, int32_t& n, int32_t& slot) {
@@ -64,30 +59,20 @@ __device__ __forceinline__ bool tree_of(const TreeArgs& a, int b, int32_t& m0, i
   return ok;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo, hi with tf32's 10 bits of mantissa (the hardware does the same to lo: 2^-21 of x is lost)
+// x = hi + lo up to 2^-22 of x: hi rounded to tf32's 10 bits of mantissa, which leaves at most 2^-11 of x to
+// lo, of which the hardware drops what is below its own 10 bits.  In integers: the conversion instruction
+// does the same for finite values and took 64 x 16 drafted tokens from 61 to 66 us, 32 x 64 from 197 to 215.
+// (An x that is not a number leaves one in lo.)
+__device__ __forceinline__ uint32_t round_tf32(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
+  hi = round_tf32(x);
   lo = __float_as_uint(x - __uint_as_float(hi));
-}
-
-// x = hi + lo up to 2^-18 of x; two values to a word, the first in the low half
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
-  const float rx = x - __uint_as_float(hi << 16), ry = y - __uint_as_float(hi & 0xffff0000u);
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(ry), "f"(rx));
 }
 
 // Up to 16 nodes, four CTAs of four warps share an SM, and each reads the state straight from L2: the
@@ -113,10 +98,7 @@ struct TreeSmem {
     struct {
       float k[kNodes][kPitch], al[kNodes][kPitch];
     };
-    struct {
-      __nv_bfloat16 hi[2 * kNodes][kPitchH], lo[2 * kNodes][kPitchH];
-    };
-    float factor[2 * kNodes][kPitchH];  // unsplit, where the parts are tf32
+    float factor[2 * kNodes][kPitchH];
   };
   // scores, zero where j is no ancestor of i; the pitch keeps 16-byte reads of neighbouring rows apart
   static constexpr int kRows = kNodes < 16 ? 16 : kNodes;
@@ -144,62 +126,40 @@ __device__ __forceinline__ float4 load_quad(const T* row, int c, int d) {
 }
 
 // 16 of the summed index times 8 columns of the right factor: a lane's four elements, 4 (lane % 4) .. + 3 of
-// the summed index, kept as two bf16 parts or as they are.
-template <bool kExact>
+// the summed index.
 struct Right {
-  uint32_t w[4];  // hi, hi, lo, lo; or four floats
-  __device__ __forceinline__ void set(float s0, float s1, float s2, float s3) {
-    if constexpr (kExact) {
-      w[0] = __float_as_uint(s0), w[1] = __float_as_uint(s1), w[2] = __float_as_uint(s2), w[3] = __float_as_uint(s3);
-    } else {
-      split2(s0, s1, w[0], w[2]);
-      split2(s2, s3, w[1], w[3]);
-    }
-  }
+  float w[4];
+  __device__ __forceinline__ void set(float s0, float s1, float s2, float s3) { w[0] = s0, w[1] = s1, w[2] = s2, w[3] = s3; }
 };
 // 16 rows of the left factor: rows lane / 4 and 8 further, the same four of the summed index
-template <bool kExact>
 struct Left {
-  uint32_t hi[kExact ? 8 : 4], lo[kExact ? 8 : 4];
+  uint32_t hi[8], lo[8];
   __device__ __forceinline__ void set(float4 x, float4 y) {
-    if constexpr (kExact) {
-      split_tf32(x.x, hi[0], lo[0]), split_tf32(y.x, hi[1], lo[1]), split_tf32(x.y, hi[2], lo[2]), split_tf32(y.y, hi[3], lo[3]);
-      split_tf32(x.z, hi[4], lo[4]), split_tf32(y.z, hi[5], lo[5]), split_tf32(x.w, hi[6], lo[6]), split_tf32(y.w, hi[7], lo[7]);
-    } else {
-      split2(x.x, x.y, hi[0], lo[0]);
-      split2(y.x, y.y, hi[1], lo[1]);
-      split2(x.z, x.w, hi[2], lo[2]);
-      split2(y.z, y.w, hi[3], lo[3]);
-    }
+    split_tf32(x.x, hi[0], lo[0]), split_tf32(y.x, hi[1], lo[1]), split_tf32(x.y, hi[2], lo[2]), split_tf32(y.y, hi[3], lo[3]);
+    split_tf32(x.z, hi[4], lo[4]), split_tf32(y.z, hi[5], lo[5]), split_tf32(x.w, hi[6], lo[6]), split_tf32(y.w, hi[7], lo[7]);
   }
 };
 // big + small += left right, the large and the small partial products apart
-template <bool kExact>
-__device__ __forceinline__ void multiply(float (&big)[4], float (&small)[4], const Left<kExact>& a, const Right<kExact>& b) {
-  if constexpr (kExact) {
+__device__ __forceinline__ void multiply(float (&big)[4], float (&small)[4], const Left& a, const Right& b) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const uint32_t ah[4] = {a.hi[4 * s], a.hi[4 * s + 1], a.hi[4 * s + 2], a.hi[4 * s + 3]};
-      const uint32_t al[4] = {a.lo[4 * s], a.lo[4 * s + 1], a.lo[4 * s + 2], a.lo[4 * s + 3]};
-      uint32_t h0, l0, h1, l1;
-      // (volatile: split anew for every tile of rows; the parts of a whole state do not fit the registers)
-      asm volatile("and.b32 %0, %1, 0xffffe000;" : "=r"(h0) : "r"(b.w[2 * s]));
-      asm volatile("and.b32 %0, %1, 0xffffe000;" : "=r"(h1) : "r"(b.w[2 * s + 1]));
-      l0 = __float_as_uint(__uint_as_float(b.w[2 * s]) - __uint_as_float(h0));
-      l1 = __float_as_uint(__uint_as_float(b.w[2 * s + 1]) - __uint_as_float(h1));
-      mma_tf32(big, ah, h0, h1);
-      mma_tf32(small, al, h0, h1);
-      mma_tf32(small, ah, l0, l1);
-    }
-  } else {
-    mma_bf16(big, a.hi, b.w[0], b.w[1]);
-    mma_bf16(small, a.lo, b.w[0], b.w[1]);
-    mma_bf16(small, a.hi, b.w[2], b.w[3]);
+  for (int s = 0; s < 2; ++s) {
+    const uint32_t ah[4] = {a.hi[4 * s], a.hi[4 * s + 1], a.hi[4 * s + 2], a.hi[4 * s + 3]};
+    const uint32_t al[4] = {a.lo[4 * s], a.lo[4 * s + 1], a.lo[4 * s + 2], a.lo[4 * s + 3]};
+    uint32_t h0, h1;
+    // (volatile: split anew for every tile of rows; the parts of a whole state do not fit the registers)
+    asm volatile("add.u32 %0, %1, 0x1000;" : "=r"(h0) : "r"(__float_as_uint(b.w[2 * s])));
+    asm volatile("add.u32 %0, %1, 0x1000;" : "=r"(h1) : "r"(__float_as_uint(b.w[2 * s + 1])));
+    h0 &= 0xffffe000u, h1 &= 0xffffe000u;
+    const uint32_t l0 = __float_as_uint(b.w[2 * s] - __uint_as_float(h0));
+    const uint32_t l1 = __float_as_uint(b.w[2 * s + 1] - __uint_as_float(h1));
+    mma_tf32(big, ah, h0, h1);
+    mma_tf32(small, al, h0, h1);
+    mma_tf32(small, ah, l0, l1);
   }
 }
 
-template <int kNodes, bool kVFirst, bool kFull, typename T, bool kExact>
-__global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ? 3 : 4) : kNodes <= 32 ? 2 : 1)
+template <int kNodes, bool kVFirst, bool kFull, typename T>
+__global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNodes <= 32 ? 2 : 1)
     tree_kernel(const TreeArgs p, const bool wide_out) {
   constexpr int kThreads = kTreeThreads<kNodes>, kWarps = kThreads / 32;
   constexpr int kCols = 8 / kWarps;  // groups of 16 value columns per warp: warp, warp + kWarps, ..
@@ -342,20 +302,8 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
       const int c = 4 * (g + kGroup * j);
       const float4 kf = make_float4(kq[j].x * w[j].x, kq[j].y * w[j].y, kq[j].z * w[j].z, kq[j].w * w[j].w);
       const float4 qf = make_float4(qq[j].x * w[j].x, qq[j].y * w[j].y, qq[j].z * w[j].z, qq[j].w * w[j].w);
-      if constexpr (kExact) {
-        *reinterpret_cast<float4*>(&sm.factor[rk][c]) = kf;
-        *reinterpret_cast<float4*>(&sm.factor[rk + 8][c]) = qf;
-      } else {
-        uint2 hi, lo;
-        split2(kf.x, kf.y, hi.x, lo.x);
-        split2(kf.z, kf.w, hi.y, lo.y);
-        *reinterpret_cast<uint2*>(&sm.hi[rk][c]) = hi;
-        *reinterpret_cast<uint2*>(&sm.lo[rk][c]) = lo;
-        split2(qf.x, qf.y, hi.x, lo.x);
-        split2(qf.z, qf.w, hi.y, lo.y);
-        *reinterpret_cast<uint2*>(&sm.hi[rk + 8][c]) = hi;
-        *reinterpret_cast<uint2*>(&sm.lo[rk + 8][c]) = lo;
-      }
+      *reinterpret_cast<float4*>(&sm.factor[rk][c]) = kf;
+      *reinterpret_cast<float4*>(&sm.factor[rk + 8][c]) = qf;
     }
   }
 
@@ -403,16 +351,9 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
           s[t][e] = c + e < dk && col + t < dv ? state[state_off(c + e, col + t, dk, dv, kVFirst)] : 0.f;
     }
   };
-  auto load_factors = [&](int tile, int ks, Left<kExact>& left) {
+  auto load_factors = [&](int tile, int ks, Left& left) {
     const int c = 16 * ks + 4 * q, r = 16 * tile + gr;
-    if constexpr (kExact) {
-      left.set(*reinterpret_cast<const float4*>(&sm.factor[r][c]), *reinterpret_cast<const float4*>(&sm.factor[r + 8][c]));
-    } else {
-      const uint2 h0 = *reinterpret_cast<const uint2*>(&sm.hi[r][c]), h1 = *reinterpret_cast<const uint2*>(&sm.hi[r + 8][c]);
-      const uint2 l0 = *reinterpret_cast<const uint2*>(&sm.lo[r][c]), l1 = *reinterpret_cast<const uint2*>(&sm.lo[r + 8][c]);
-      left.hi[0] = h0.x, left.hi[1] = h1.x, left.hi[2] = h0.y, left.hi[3] = h1.y;
-      left.lo[0] = l0.x, left.lo[1] = l1.x, left.lo[2] = l0.y, left.lo[3] = l1.y;
-    }
+    left.set(*reinterpret_cast<const float4*>(&sm.factor[r][c]), *reinterpret_cast<const float4*>(&sm.factor[r + 8][c]));
   };
   // accumulator n = 2 (lane % 4) + {0, 1} of n-tile nt is column 16 group + 2 n + nt
   auto put = [&](int tile, int group, const float (&big)[2][4], const float (&small)[2][4]) {
@@ -424,7 +365,7 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
   };
   if constexpr (kStaged<kNodes>) {
     static_assert(kCols == 1, "a warp takes one group");
-    Right<kExact> right[8][2];  // [k-step][n-tile]
+    Right right[8][2];  // [k-step][n-tile]
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
       float s[2][4];
@@ -438,16 +379,15 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
       float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        Left<kExact> left;
+        Left left;
         load_factors(t, ks, left);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) multiply<kExact>(big[nt], small[nt], left, right[ks][nt]);
+        for (int nt = 0; nt < 2; ++nt) multiply(big[nt], small[nt], left, right[ks][nt]);
       }
       put(t, warp, big, small);
     }
   } else {
-    // few rows: all of them are accumulated while the state streams by, a k-step ahead (1: 54.3 us at 64
-    // sequences of up to 16 nodes and 32 heads, 2: 55.1, 3: 55.8, 4: 60.2; one group of columns after the other: 58)
+    // few rows: all of them are accumulated while the state streams by, a k-step ahead
     constexpr int kTiles = kNodes / 8, kAhead = 1;
     float s[kAhead + 1][kCols][2][4], big[kTiles][kCols][2][4] = {}, small[kTiles][kCols][2][4] = {};
 #pragma unroll
@@ -461,7 +401,7 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
 #pragma unroll
         for (int g = 0; g < kCols; ++g) load_state(warp + kWarps * g, ks + kAhead, s[(ks + kAhead) % (kAhead + 1)][g]);
       }
-      Left<kExact> left[kTiles];
+      Left left[kTiles];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) load_factors(t, ks, left[t]);
 #pragma unroll
@@ -469,10 +409,10 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           const float(&w)[4] = s[ks % (kAhead + 1)][g][nt];
-          Right<kExact> right;
+          Right right;
           right.set(w[0], w[1], w[2], w[3]);
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) multiply<kExact>(big[t][g][nt], small[t][g][nt], left[t], right);
+          for (int t = 0; t < kTiles; ++t) multiply(big[t][g][nt], small[t][g][nt], left[t], right);
         }
     }
 #pragma unroll
@@ -490,7 +430,7 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
   float* deltas = p.deltas + ((size_t)m0 * p.Hv + h) * dv;
   bool walk = false;
   constexpr int kBlocks = (kNodes + 15) / 16;
-  Right<kExact> solved[kCols][kBlocks][2];  // solved blocks as fragments: [.][block][n-tile]
+  Right solved[kCols][kBlocks][2];  // solved blocks as fragments: [.][block][n-tile]
   if constexpr (kNodes < 64) load_values(0);
 #pragma unroll
   for (int blk = 0; blk < kBlocks; ++blk) {
@@ -501,11 +441,11 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
       float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
       for (int kb = 0; kb < blk; ++kb) {
-        Left<kExact> left;
+        Left left;
         left.set(*reinterpret_cast<const float4*>(&sm.a[i0 + gr][16 * kb + 4 * q]),
                  *reinterpret_cast<const float4*>(&sm.a[i0 + gr + 8][16 * kb + 4 * q]));
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) multiply<kExact>(big[nt], small[nt], left, solved[g][kb][nt]);
+        for (int nt = 0; nt < 2; ++nt) multiply(big[nt], small[nt], left, solved[g][kb][nt]);
       }
       float4* r0 = reinterpret_cast<float4*>(&sm.u[i0 + gr][c0(g)]);
       float4* r8 = reinterpret_cast<float4*>(&sm.u[i0 + gr + 8][c0(g)]);
@@ -593,11 +533,11 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? (kExact ?
         float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
         for (int kb = 0; kb <= blk; ++kb) {
-          Left<kExact> left;
+          Left left;
           left.set(*reinterpret_cast<const float4*>(&sm.b[i0 + gr][16 * kb + 4 * q]),
                    *reinterpret_cast<const float4*>(&sm.b[i0 + gr + 8][16 * kb + 4 * q]));
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) multiply<kExact>(big[nt], small[nt], left, solved[g][kb][nt]);
+          for (int nt = 0; nt < 2; ++nt) multiply(big[nt], small[nt], left, solved[g][kb][nt]);
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -756,15 +696,12 @@ cudaError_t pick(const TreeArgs& a, cudaStream_t stream) {
     // the form for 128 x 128 states reads rows in wide accesses: all of them start on 16 bytes (bf16: 8)
     const size_t in = a.in_bf16 ? 8 : 16;
     const bool wide = full && on(a.q, in) && on(a.k, in) && on(a.v, in) && on(a.raw_gate, 16) && on(a.dt_bias, 16);
-    auto layout = [&](auto type, auto exact) {
+    auto layout = [&](auto type) {
       using T = decltype(type);
-      constexpr bool kExact = decltype(exact)::value;
-      if (a.v_first)
-        return wide ? go(tree_kernel<kNodes, true, true, T, kExact>) : go(tree_kernel<kNodes, true, false, T, kExact>);
-      return wide ? go(tree_kernel<kNodes, false, true, T, kExact>) : go(tree_kernel<kNodes, false, false, T, kExact>);
+      if (a.v_first) return wide ? go(tree_kernel<kNodes, true, true, T>) : go(tree_kernel<kNodes, true, false, T>);
+      return wide ? go(tree_kernel<kNodes, false, true, T>) : go(tree_kernel<kNodes, false, false, T>);
     };
-    if (!a.in_bf16) return layout(float{}, std::true_type{});
-    return a.out_bf16 ? layout(__nv_bfloat16{}, std::false_type{}) : layout(__nv_bfloat16{}, std::true_type{});
+    return a.in_bf16 ? layout(__nv_bfloat16{}) : layout(float{});
   }
 }
 
