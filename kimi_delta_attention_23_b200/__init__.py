@@ -275,44 +275,50 @@ def _launch(index, call, *args):
         return call(*args)
 
 
-def _used_on(stream, index, *tensors):
-    """Tells the allocator that tensors made here are in use on ``stream`` (see _Owned)."""
-    if stream is not None and stream != torch.cuda.current_stream(index):
+# PyTorch's caching allocator ties a block to the stream that was current when it was allocated: a block
+# freed on that stream is handed out again at once, since whatever still uses it there comes first.  Kernels
+# on another stream do not wait for that, so what a wrapper makes itself for a call with ``stream`` (results
+# and scratch) is allocated with ``stream`` current; and the results, which the caller goes on to use on its
+# own current stream, are marked as in use there (``record_stream``), so that freeing them waits for both.
+def _elsewhere(stream, device):
+    """Whether the call's kernels run on another stream than the current one."""
+    return stream is not None and stream != torch.cuda.current_stream(device)
+
+
+def _make(stream, device, make, /, *args, **kw):
+    """make(...), a tensor that kernels on ``stream`` may write at once."""
+    if not _elsewhere(stream, device):
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _hand_over(stream, device, *tensors):
+    """Results of _make that the caller gets, on its way out of the call."""
+    if _elsewhere(stream, device):
+        current = torch.cuda.current_stream(device)
         for t in tensors:
             if t is not None and t.numel():
-                t.record_stream(stream)
+                t.record_stream(current)
 
 
 class _Owned:
-    """Device tensors a wrapper allocates itself (results and scratch).
-
-    PyTorch's caching allocator ties a block to the stream that was current when it was
-    allocated.  The kernels run on ``stream``; when that is another stream, every such tensor is
-    marked as in use there (``record_stream``), so that its memory goes to other work only after
-    the kernels on ``stream`` are done with it -- the scratch a wrapper drops at return as much as
-    a result the caller frees later."""
+    """Device tensors a wrapper makes itself (results and scratch), as _make and _hand_over do."""
 
     def __init__(self, stream, device):
         self.stream, self.device, self.tensors = stream, device, []
 
     def empty(self, *shape, **kw):
-        t = torch.empty(*shape, **kw)
+        t = _make(self.stream, self.device, torch.empty, *shape, **kw)
         self.tensors.append(t)
         return t
 
-    def keep(self, t, original=None):
-        # a temporary made from a caller's tensor (.contiguous() and the like); the caller's own
-        # tensor is left alone
-        if original is None or t.data_ptr() != original.data_ptr():
-            self.tensors.append(t)
-        return t
+    def contiguous(self, t):
+        # the copy of a tensor that is not contiguous is read on ``stream``, so it is written there
+        return t if t.is_contiguous() else _make(self.stream, self.device, t.contiguous)
 
     def launched(self):
-        if self.stream is None or self.stream == torch.cuda.current_stream(self.device):
-            return
-        for t in self.tensors:
-            if t.numel() and t.device.type == "cuda":
-                t.record_stream(self.stream)
+        _hand_over(self.stream, self.device, *self.tensors)
 
 
 def kda_chunk_fwd(q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool, state_indices,
@@ -578,7 +584,7 @@ def kda_context_parallel(transition_matrices, local_contributions, initial_state
     if method not in ("auto", "sequential", "logdepth"):
         raise ValueError(f"unknown scan method {method!r}")
     own = _Owned(stream, S0.device)
-    Mc, Uc, Sc = own.keep(M.contiguous(), M), own.keep(U.contiguous(), U), own.keep(S0.contiguous(), S0)
+    Mc, Uc, Sc = own.contiguous(M), own.contiguous(U), own.contiguous(S0)
     N, H, dk = M.shape[0], M.shape[1], M.shape[-1]
     dv = U.shape[-1] if state_layout == "K_FIRST" else U.shape[-2]
     ws = None

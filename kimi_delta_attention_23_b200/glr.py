@@ -19,8 +19,8 @@ import ctypes
 
 import torch
 
-from . import (_checker, _DTYPES, KdaError, _dev, _flags, _launch, _need, _need_rank, _on_stream, _used_on, _where,
-               load_library)
+from . import (_checker, _DTYPES, KdaError, _dev, _flags, _hand_over, _launch, _make, _need, _need_rank, _on_stream,
+               _where, load_library)
 
 __all__ = ["kda_glr_fwd", "kda_glr_bwd", "kda_glr_decode", "kda_glr_checkpoint_shape", "kda_glr_bwd_workspace_size"]
 
@@ -94,14 +94,14 @@ def _pool(state_pool, state_indices, like, index, B, H, d):
     return at, shape[0], _need(state_indices, "state_indices", torch.int32, (B,), like, index)
 
 
-def _output(out, output_dtype, x, index):
+def _output(out, output_dtype, x, index, stream):
     """The output (made here if ``out`` is None), its address and type."""
     if output_dtype is None:
         output_dtype = x.dtype if out is None else out.dtype
     if output_dtype not in _DTYPES or (x.dtype is torch.float32 and output_dtype is not torch.float32):
         raise ValueError("output_dtype must be float32, or bfloat16 beside a bfloat16 x")
     if out is None:
-        out = torch.empty_like(x, dtype=output_dtype)
+        out = _make(stream, index, torch.empty_like, x, dtype=output_dtype)
         return out, out.data_ptr(), _DTYPES[output_dtype]
     return out, _need(out, "out", output_dtype, x.shape, x, index), _DTYPES[output_dtype]
 
@@ -132,11 +132,11 @@ def kda_glr_fwd(x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, state_pool
     if checkpoints is not None:
         kept = _need(checkpoints, "checkpoints", torch.float32, (lib.kda_glr_checkpoints(T, B), H, d), x, index)
     status, given = _status(device_status, x, index), out
-    out, to, out_type = _output(out, output_dtype, x, index)
+    out, to, out_type = _output(out, output_dtype, x, index, stream)
     rc = _launch(index, lib.kda_glr_fwd, xs, x_type, raws, gate_type, betas, a_logs, biases, cu, B, T, H, d, pool, slots,
                  indices, to, out_type, kept, flags, gate_lower_bound, status, _on_stream(stream, index))
-    if given is None and stream is not None:
-        _used_on(stream, index, out)
+    if given is None:
+        _hand_over(stream, index, out)
     if rc != 0:
         raise KdaError(rc, "kda_glr_fwd")
     return out
@@ -154,11 +154,11 @@ def kda_glr_decode(x, raw_gate, beta_logits, a_log, dt_bias, state_pool, state_i
     else:
         index, B, H, d, slots, xs, raws, betas, a_logs, biases, pool, indices, x_type, gate_type = found
     status, given = _status(device_status, x, index), out
-    out, to, out_type = _output(out, output_dtype, x, index)
+    out, to, out_type = _output(out, output_dtype, x, index, stream)
     rc = _launch(index, lib.kda_glr_decode, xs, x_type, raws, gate_type, betas, a_logs, biases, B, H, d, pool, slots, indices,
                  to, out_type, flags, gate_lower_bound, status, _on_stream(stream, index))
-    if given is None and stream is not None:
-        _used_on(stream, index, out)
+    if given is None:
+        _hand_over(stream, index, out)
     if rc != 0:
         raise KdaError(rc, "kda_glr_decode")
     return out
@@ -193,7 +193,7 @@ def kda_glr_bwd(dout, x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, chec
 
     def grad(t, name, shape, dtype=torch.float32):
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=x.device)
+            t = _make(stream, index, torch.empty, shape, dtype=dtype, device=x.device)
             made.append(t)
             return t, t.data_ptr()
         return t, _need(t, name, dtype, shape, x, index)
@@ -206,13 +206,12 @@ def kda_glr_bwd(dout, x, raw_gate, beta_logits, a_log, dt_bias, cu_seqlens, chec
     d_initial, dis = grad(d_initial, "d_initial", (B, H, d))
     if workspace is None:
         need = _launch(index, lib.kda_glr_bwd_workspace_size, T, B, H, d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        made.append(workspace)
+        workspace = _make(stream, index, torch.empty, need, dtype=torch.uint8, device=x.device)
     _dev(workspace, "workspace", torch.uint8, x.device)
     rc = _launch(index, lib.kda_glr_bwd, douts, _DTYPES[dtype], *inputs, cu, B, T, H, d, kept, final, dxs, draws, dbetas, das,
                  dbs, dis, flags, gate_lower_bound, workspace.data_ptr(), workspace.numel(), status,
                  _on_stream(stream, index))
-    _used_on(stream, index, *made)
+    _hand_over(stream, index, *made)
     if rc != 0:
         raise KdaError(rc, "kda_glr_bwd")
     return {"dx": dx, "draw_gate": draw_gate, "dbeta": dbeta, "da_log": da_log, "ddt_bias": ddt_bias,

@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import KdaError, _dev, _launch, _need, _need_rank, _on_stream, _used_on, load_library
+from . import KdaError, _dev, _hand_over, _launch, _make, _need, _need_rank, _on_stream, load_library
 
 __all__ = ["kda_pool_copy", "kda_pool_fork", "kda_pool_free", "kda_pool_compact", "kda_pool_workspace_size",
            "MAX_POOL_COPIES"]
@@ -61,13 +61,12 @@ def _call(what, pool, layout, lists, n, results, workspace, device_status, strea
     if workspace is not None:
         _dev(workspace, "workspace", torch.uint8, pool.device)
     elif what != "kda_pool_copy" or n > FEW_COPIES:
-        workspace = torch.empty(lib.kda_pool_workspace_size(n, slots), dtype=torch.uint8, device=pool.device)
-        made = (*made, workspace)
+        need = lib.kda_pool_workspace_size(n, slots)
+        workspace = _make(stream, index, torch.empty, need, dtype=torch.uint8, device=pool.device)
     at, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     rc = _launch(index, getattr(lib, what), pool.data_ptr(), layers, slots, elems, *lists, n, *results, at, size, status,
                  _on_stream(stream, index))
-    if stream is not None:
-        _used_on(stream, index, *made)
+    _hand_over(stream, index, *made)
     if rc != 0:
         raise KdaError(rc, what)
 
@@ -97,7 +96,7 @@ def kda_pool_fork(state_pool, live, src, dst=None, *, stacked=False, workspace=N
     n, srcs = _list(src, "src", state_pool, index)
     made = ()
     if dst is None:
-        dst = torch.empty_like(src)
+        dst = _make(stream, index, torch.empty_like, src)
         made = (dst,)
     _, dsts = _list(dst, "dst", state_pool, index, n)
     _call("kda_pool_fork", state_pool, layout, (lives, srcs, dsts), n, (), workspace, device_status, stream, made)
@@ -129,7 +128,7 @@ def kda_pool_compact(state_pool, live, state_indices, num_live=None, *, stacked=
     n, indices = _list(state_indices, "state_indices", state_pool, index)
     made = ()
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=state_pool.device)
+        num_live = _make(stream, index, torch.empty, 1, dtype=torch.int32, device=state_pool.device)
         made = (num_live,)
     _, counts = _list(num_live, "num_live", state_pool, index, 1)
     _call("kda_pool_compact", state_pool, layout, (lives, indices), n, (counts,), workspace, device_status, stream, made)

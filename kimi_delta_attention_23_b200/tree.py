@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from . import (_checker, _DTYPES, KdaError, _flags, _launch, _need, _need_rank, _on_stream, _used_on, _where,
+from . import (_checker, _DTYPES, KdaError, _flags, _hand_over, _launch, _make, _need, _need_rank, _on_stream, _where,
                load_library)
 
 __all__ = ["kda_tree_decode", "kda_tree_commit", "MAX_TREE_NODES"]
@@ -107,16 +107,15 @@ def kda_tree_decode(q, k, v, raw_gate, beta_logits, a_log, dt_bias, cu_nodes, pa
     status = None if device_status is None else _need(device_status, "device_status", torch.int32, (1,), q, index)
     new_out, new_deltas = out is None, deltas is None
     if new_out:
-        out = torch.empty_like(v, dtype=output_dtype)
+        out = _make(stream, index, torch.empty_like, v, dtype=output_dtype)
     if new_deltas:
-        deltas = torch.empty_like(v, dtype=torch.float32)
+        deltas = _make(stream, index, torch.empty_like, v, dtype=torch.float32)
     rc = _launch(index, lib.kda_tree_decode, qs, ks, vs, in_type, raws, betas, alogs, biases, cu, pars, B, M, max_nodes, Hk,
                  Hv, dk, dv, pool, slots, indices,
                  out.data_ptr() if new_out else _need(out, "out", output_dtype, (M, Hv, dv), q, index), _DTYPES[output_dtype],
                  deltas.data_ptr() if new_deltas else _need(deltas, "deltas", torch.float32, (M, Hv, dv), q, index), flags,
                  gate_lower_bound, status, _on_stream(stream, index))
-    if stream is not None:
-        _used_on(stream, index, out if new_out else None, deltas if new_deltas else None)
+    _hand_over(stream, index, out if new_out else None, deltas if new_deltas else None)
     if rc != 0:
         raise KdaError(rc, "kda_tree_decode")
     return out, deltas
