@@ -102,13 +102,14 @@ enum {
   KDA_SCAN_LOGDEPTH = 1u << 7, /* segment call: the scan in log depth (needs the workspace of
                                   kda_scan_workspace_size); without it the log-depth form is
                                   chosen when that workspace is given and it is expected faster */
-  KDA_DEBUG_WITHHOLD_HANDOFF = 1u << 8, /* test hook for the bounded waits (kda_chunk_fwd): the bf16
+  KDA_DEBUG_WITHHOLD_HANDOFF = 1u << 8, /* test hook for the bounded waits.  kda_chunk_fwd: the bf16
                                   kernel withholds one "scores ready" signal between its two
                                   warp teams in every chain's first chunk, so the waiting team
-                                  gives up after its limit (about one second).  device_status
-                                  then reads KDA_ERR_DEVICE_TIMEOUT, the outputs and the pool
-                                  slots are unspecified, and the context stays usable.  No
-                                  effect on the fp32 kernel. */
+                                  gives up after its limit (about one second).  No effect on the
+                                  fp32 kernel.  kda_glr_fwd, kda_glr_bwd: the last CTA of every
+                                  chain's cluster withholds its first map from the others.
+                                  device_status then reads KDA_ERR_DEVICE_TIMEOUT, the outputs and
+                                  the pool slots are unspecified, and the context stays usable. */
   KDA_INPUT_NORM = 1u << 9     /* kda_glr_*: the input is scaled by sqrt(1 - a^2)                */
 };
 

@@ -200,13 +200,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
   cluster.sync();
   auto wait = [&](uint64_t* bar, int parity) {
     const uint32_t at = sm100::smem_addr(bar);
-    if (sm100::mbar_try_wait(at, parity & 1)) return;  // nearly always: a sleeping wait takes longer to say so
-    // one wait that ran out is the CTA's last: its threads then run through to the end
+    if (sm100::mbar_try_wait(at, parity & 1)) return true;  // nearly always: a sleeping wait takes longer to say so
+    // one wait that ran out is the CTA's last: its threads then run through to the end, sending and fetching
+    // nothing more
     volatile int* gave_up = &sm.gave_up;
-    if (*gave_up || sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) return;
+    if (*gave_up) return false;
+    if (sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) return true;
     *gave_up = 1;
     report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    return false;
   };
+  // Nothing of a CTA may be under way to its shared memory when it ends, nor anything of the others': before the
+  // cluster's closing barrier the issuing thread waits, even after another wait has run out and again with a
+  // limit, for the copies it has started.
+  auto drain = [&](int fetched) {
+    if (how == kTensor && threadIdx.x == 32 * kFwdWarps)
+      for (int s = max(0, min(fetched, steps) - kStages); s < min(fetched, steps); ++s)
+        sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full[s % kStages]), s / kStages & 1, kWaitNs);
+    __syncwarp();
+  };
+  const bool withhold = (p.flags & KDA_DEBUG_WITHHOLD_HANDOFF) && rank == ranks - 1;
 
   const int pitch = how == kTensor ? d : kRow;  // elements of a tile's row
 
@@ -224,11 +237,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
       sm100::tma_load_3d(sm100::smem_addr(sm.raw[stage]), &maps.raw, 0, h, t, bar);
     };
     for (int s = 0; s < kStages; ++s) fetch(s);
+    int fetched = kStages;
+    bool live = true;
     float* state = p.pool + ((size_t)slot * p.H + h) * d;
     float carry = c < d ? state[c] : 0.f;
     for (int step = 0; step < steps; ++step) {
       const int par = step & 1;
-      wait(&sm.mapped[par], step >> 1);
+      live &= wait(&sm.mapped[par], step >> 1);
       float2 of[kFwdWarps];
       float pa = 1.f, pb = 0.f;
 #pragma unroll
@@ -238,11 +253,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
         pb = fmaf(pb, of[w].x, of[w].y);
         pa *= of[w].x;
       }
-      for (int k = 0; k < ranks; ++k) send_map(&sm.tile_map[par][rank][c], &sm.tiles_in[par], k, pa, pb);
-      if (c == 0)
-        sm100::mbar_arrive_expect_tx(sm100::smem_addr(&sm.tiles_in[par]), ranks * kRow * (uint32_t)sizeof(float2));
-      fetch(step + kStages);  // into the tile that has just been read
-      wait(&sm.tiles_in[par], step >> 1);
+      if (live) {
+        if (!(withhold && step == 0))
+          for (int k = 0; k < ranks; ++k) send_map(&sm.tile_map[par][rank][c], &sm.tiles_in[par], k, pa, pb);
+        if (c == 0)
+          sm100::mbar_arrive_expect_tx(sm100::smem_addr(&sm.tiles_in[par]), ranks * kRow * (uint32_t)sizeof(float2));
+        fetch(step + kStages);  // into the tile that has just been read
+        fetched = step + kStages + 1;
+      }
+      live &= wait(&sm.tiles_in[par], step >> 1);
       float in = carry;
       float2 m[kMaxCluster];
 #pragma unroll
@@ -264,6 +283,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
       if (lane == 0) sm100::mbar_arrive(sm100::smem_addr(&sm.entered[par]));
     }
     if (rank == 0 && c < d) state[c] = carry;
+    drain(fetched);
+    sm100::cluster_arrive();
+    sm100::cluster_wait();
     return;
   }
 
@@ -408,7 +430,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
     if (step + 2 < steps) work_out(step + 2, even);
     finish(step + 1, odd);
   }
+  __syncwarp();
+  sm100::cluster_arrive_relaxed();  // a computing warp touches no other CTA's memory
   sm100::bulk_wait_all();
+  sm100::cluster_wait();
 }
 
 // ------------------------------------------------------------------------------------ backward
@@ -500,13 +525,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   cluster.sync();
   auto wait = [&](uint64_t* bar, int parity) {
     const uint32_t at = sm100::smem_addr(bar);
-    if (sm100::mbar_try_wait(at, parity & 1)) return;  // nearly always: a sleeping wait takes longer to say so
-    // one wait that ran out is the CTA's last: its threads then run through to the end
+    if (sm100::mbar_try_wait(at, parity & 1)) return true;  // nearly always: a sleeping wait takes longer to say so
+    // one wait that ran out is the CTA's last: its threads then run through to the end, sending and fetching
+    // nothing more
     volatile int* gave_up = &sm.gave_up;
-    if (*gave_up || sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) return;
+    if (*gave_up) return false;
+    if (sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) return true;
     *gave_up = 1;
     report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    return false;
   };
+  // as in the forward pass
+  auto drain = [&](int fetched) {
+    if (how == kTensor && threadIdx.x == 32 * kBwdWarps)
+      for (int s = max(0, min(fetched, steps) - kStages); s < min(fetched, steps); ++s)
+        sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full[s % kStages]), s / kStages & 1, kWaitNs);
+    __syncwarp();
+  };
+  const bool withhold = (p.flags & KDA_DEBUG_WITHHOLD_HANDOFF) && rank == ranks - 1;
 
   if (warp >= kBwdWarps) {
     // ---------------------------------------------------------------- carrying warps
@@ -522,6 +558,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       sm100::tma_load_3d(sm100::smem_addr(sm.dout[stage]), &maps.dout, 0, h, t, bar);
     };
     for (int s = 0; s < kStages - 1; ++s) fetch(s);
+    int fetched = kStages - 1;
+    bool live = true;
     const float* kept = p.checkpoints + ((size_t)(s0 / kTile + b) * p.H + h) * d + c;
     auto entering = [&](int step) {
       const int tile = tile_of(step);
@@ -532,7 +570,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     float state = entering(0);
     for (int step = 0; step < steps; ++step) {
       const int par = step & 1, buf = kAhead ? par : 0;
-      wait(&sm.mapped[par], step >> 1);
+      live &= wait(&sm.mapped[par], step >> 1);
       float2 of[kBwdWarps];
       float back[kBwdWarps], pa = 1.f, pb = 0.f;
 #pragma unroll
@@ -545,9 +583,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         pb = fmaf(pb, of[w].x, back[w]);
         pa *= of[w].x;
       }
-      for (int k = 0; k < ranks; ++k) send_map(&sm.tile_map[par][rank][c], &sm.tiles_in[par], k, pa, pb);
-      if (c == 0)
-        sm100::mbar_arrive_expect_tx(sm100::smem_addr(&sm.tiles_in[par]), ranks * kRow * (uint32_t)sizeof(float2));
+      if (live) {
+        if (!(withhold && step == 0))
+          for (int k = 0; k < ranks; ++k) send_map(&sm.tile_map[par][rank][c], &sm.tiles_in[par], k, pa, pb);
+        if (c == 0)
+          sm100::mbar_arrive_expect_tx(sm100::smem_addr(&sm.tiles_in[par]), ranks * kRow * (uint32_t)sizeof(float2));
+      }
 #pragma unroll
       for (int w = 0; w < kBwdWarps; ++w) {  // the state entering each warp's tokens, over B
         const float in = state;
@@ -555,7 +596,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         of[w].y = in;
       }
       state = entering(step + 1);
-      wait(&sm.tiles_in[par], step >> 1);
+      live &= wait(&sm.tiles_in[par], step >> 1);
       float in = carry;
       float2 m[kMaxCluster];
 #pragma unroll
@@ -573,11 +614,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(sm100::smem_addr(&sm.entered[par]));
       // the next tile goes where the last step's gradients have left
-      if (step > 0 && c == 0) wait(&sm.done[(step - 1) & 1], (step - 1) >> 1);
-      fetch(step + kStages - 1);
+      if (step > 0 && c == 0) live &= wait(&sm.done[(step - 1) & 1], (step - 1) >> 1);
+      if (live) {
+        fetch(step + kStages - 1);
+        fetched = step + kStages;
+      }
     }
     if (rank == 0 && c < d) p.d_initial[at] = carry;
-    __syncwarp();
+    drain(fetched);
+    sm100::cluster_arrive();
   } else {
     // ---------------------------------------------------------------- computing warps
     const HeadGate gate = head_gate(p.a_log[h], kSafe, p.lb);
@@ -818,6 +863,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
     }
+    __syncwarp();
+    sm100::cluster_arrive_relaxed();  // a computing warp touches no other CTA's memory
     sm100::bulk_wait_all();
     // ---- the warp's share of the parameters' gradients
     float* red = &sm.rev[0][0][0];  // [warps][kRow]
@@ -836,6 +883,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       part[i] = i < d ? s : s * kLn2;  // the last one: dg g, g having been kept times log2 e
     }
   }
+  __syncwarp();
+  sm100::cluster_wait();
 }
 
 // ddt_bias and da_log from the partial sums: one warp per (head, channel or the head's own sum),

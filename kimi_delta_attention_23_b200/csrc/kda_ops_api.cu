@@ -7,7 +7,8 @@
 
 namespace {
 
-constexpr uint32_t kGlrFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_INPUT_NORM;
+constexpr uint32_t kGlrDecodeFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_INPUT_NORM;
+constexpr uint32_t kGlrFlags = kGlrDecodeFlags | KDA_DEBUG_WITHHOLD_HANDOFF;
 constexpr uint32_t kTreeFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_STATE_V_FIRST;
 constexpr int64_t kMaxTokens = INT32_MAX - 1024;  // the recurrence counts in whole tiles past the end
 constexpr int32_t kMaxNodes = 64;
@@ -92,7 +93,7 @@ extern "C" kda_status_t kda_glr_decode(const void* x, kda_dtype_t x_dtype, const
                                        kda_dtype_t out_dtype, uint32_t flags, float gate_lower_bound,
                                        int32_t* device_status, void* stream) {
   if (batch < 0 || num_heads <= 0 || d <= 0 || max_slots <= 0) return KDA_ERR_INVALID_ARG;
-  if ((flags & ~kGlrFlags) != 0) return KDA_ERR_INVALID_ARG;
+  if ((flags & ~kGlrDecodeFlags) != 0) return KDA_ERR_INVALID_ARG;
   if (!state_pool || !state_indices || !a_log || !dt_bias) return KDA_ERR_INVALID_ARG;
   if (batch > 0 && (!x || !raw_gate || !beta_logits || !out)) return KDA_ERR_INVALID_ARG;
   if (kda_status_t s = glr_types(x_dtype, gate_dtype, out_dtype); s != KDA_OK) return s;

@@ -94,6 +94,15 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t addr, uint32_t by
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes) : "memory");
 }
 
+// ---------------------------------------------------------------- cluster barrier
+// Arrival and wait apart: a thread that has nothing more to do with the other CTAs' memory arrives early.
+// All lanes of a warp together.  The relaxed form orders none of the thread's own accesses.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // ---------------------------------------------------------------- bulk copy engine
 // contiguous global -> shared copy (16-byte aligned addresses, size a multiple of 16),
 // completion counted in bytes on the mbarrier
