@@ -123,6 +123,21 @@ __device__ __forceinline__ bool sequence(const int32_t* cu, int b, int64_t T, in
   return s0 >= 0 && n >= 0 && (int64_t)s0 + n <= T;
 }
 
+// A wait with a limit; kOthers where the cluster's other CTAs write what is waited for.  One that ran out is
+// the CTA's last: its threads then run through to the end, sending and fetching nothing more.
+template <bool kOthers>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* gave_up, int32_t* status) {
+  const uint32_t at = sm100::smem_addr(bar);
+  // nearly always there: a sleeping wait takes longer to say so
+  if (kOthers ? sm100::mbar_try_wait_cluster(at, parity) : sm100::mbar_try_wait(at, parity)) return true;
+  if (*gave_up) return false;
+  if (kOthers ? sm100::mbar_wait_sleep_cluster(at, parity, kWaitNs) : sm100::mbar_wait_sleep(at, parity, kWaitNs))
+    return true;
+  *gave_up = 1;
+  report(status, KDA_ERR_DEVICE_TIMEOUT);
+  return false;
+}
+
 // A pair to the same place in the shared memory of CTA `rank` of the cluster, counted on that CTA's
 // barrier.  The message orders itself: a cluster barrier would make every thread wait until its
 // outputs have been written to global memory.
@@ -198,18 +213,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
     sm.gave_up = 0;
   }
   cluster.sync();
-  auto wait = [&](uint64_t* bar, int parity) {
-    const uint32_t at = sm100::smem_addr(bar);
-    if (sm100::mbar_try_wait(at, parity & 1)) return true;  // nearly always: a sleeping wait takes longer to say so
-    // one wait that ran out is the CTA's last: its threads then run through to the end, sending and fetching
-    // nothing more
-    volatile int* gave_up = &sm.gave_up;
-    if (*gave_up) return false;
-    if (sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) return true;
-    *gave_up = 1;
-    report(p.status, KDA_ERR_DEVICE_TIMEOUT);
-    return false;
-  };
+  auto wait = [&](uint64_t* bar, int parity) { return wait_for<false>(bar, parity & 1, &sm.gave_up, p.status); };
+  auto wait_others = [&](uint64_t* bar, int parity) { return wait_for<true>(bar, parity & 1, &sm.gave_up, p.status); };
   // Nothing of a CTA may be under way to its shared memory when it ends, nor anything of the others': before the
   // cluster's closing barrier the issuing thread waits, even after another wait has run out and again with a
   // limit, for the copies it has started.
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
         fetch(step + kStages);  // into the tile that has just been read
         fetched = step + kStages + 1;
       }
-      live &= wait(&sm.tiles_in[par], step >> 1);
+      live &= wait_others(&sm.tiles_in[par], step >> 1);
       float in = carry;
       float2 m[kMaxCluster];
 #pragma unroll
@@ -282,10 +287,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) glr_fwd_kernel(const GlrArgs p
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(sm100::smem_addr(&sm.entered[par]));
     }
-    if (rank == 0 && c < d) state[c] = carry;
     drain(fetched);
     sm100::cluster_arrive();
     sm100::cluster_wait();
+    // after the barrier: every CTA of the cluster has read the state that this replaces
+    if (rank == 0 && c < d) state[c] = carry;
     return;
   }
 
@@ -523,18 +529,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       reinterpret_cast<uint4*>(&sm)[i] = make_uint4(0, 0, 0, 0);
   }
   cluster.sync();
-  auto wait = [&](uint64_t* bar, int parity) {
-    const uint32_t at = sm100::smem_addr(bar);
-    if (sm100::mbar_try_wait(at, parity & 1)) return true;  // nearly always: a sleeping wait takes longer to say so
-    // one wait that ran out is the CTA's last: its threads then run through to the end, sending and fetching
-    // nothing more
-    volatile int* gave_up = &sm.gave_up;
-    if (*gave_up) return false;
-    if (sm100::mbar_wait_sleep(at, parity & 1, kWaitNs)) return true;
-    *gave_up = 1;
-    report(p.status, KDA_ERR_DEVICE_TIMEOUT);
-    return false;
-  };
+  auto wait = [&](uint64_t* bar, int parity) { return wait_for<false>(bar, parity & 1, &sm.gave_up, p.status); };
+  auto wait_others = [&](uint64_t* bar, int parity) { return wait_for<true>(bar, parity & 1, &sm.gave_up, p.status); };
   // as in the forward pass
   auto drain = [&](int fetched) {
     if (how == kTensor && threadIdx.x == 32 * kBwdWarps)
@@ -596,7 +592,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         of[w].y = in;
       }
       state = entering(step + 1);
-      live &= wait(&sm.tiles_in[par], step >> 1);
+      live &= wait_others(&sm.tiles_in[par], step >> 1);
       float in = carry;
       float2 m[kMaxCluster];
 #pragma unroll
