@@ -108,6 +108,8 @@ enum {
                                   gives up after its limit (about one second).  No effect on the
                                   fp32 kernel.  kda_glr_fwd, kda_glr_bwd: the last CTA of every
                                   chain's cluster withholds its first map from the others.
+                                  kda_tree_decode: the copy of a 128 x 128 state to trees of more
+                                  than 16 nodes is not started (no effect on other forms).
                                   device_status then reads KDA_ERR_DEVICE_TIMEOUT, the outputs and
                                   the pool slots are unspecified, and the context stays usable. */
   KDA_INPUT_NORM = 1u << 9     /* kda_glr_*: the input is scaled by sqrt(1 - a^2)                */

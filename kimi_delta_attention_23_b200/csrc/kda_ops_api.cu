@@ -9,7 +9,7 @@ namespace {
 
 constexpr uint32_t kGlrDecodeFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_INPUT_NORM;
 constexpr uint32_t kGlrFlags = kGlrDecodeFlags | KDA_DEBUG_WITHHOLD_HANDOFF;
-constexpr uint32_t kTreeFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_STATE_V_FIRST;
+constexpr uint32_t kTreeFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_STATE_V_FIRST | KDA_DEBUG_WITHHOLD_HANDOFF;
 constexpr int64_t kMaxTokens = INT32_MAX - 1024;  // the recurrence counts in whole tiles past the end
 constexpr int32_t kMaxNodes = 64;
 constexpr int32_t kMaxCopies = 8192;  // pairs of one simultaneous copy: 16 bytes of each fit shared memory

@@ -188,8 +188,10 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
       const uint32_t bar = sm100::smem_addr(&sm.full);
       sm100::mbar_init(bar, 1);
       sm100::fence_mbar_init();
-      sm100::mbar_arrive_expect_tx(bar, sizeof(sm.state));
-      sm100::bulk_g2s(sm100::smem_addr(sm.state), state, sizeof(sm.state), bar);
+      if (!(p.flags & KDA_DEBUG_WITHHOLD_HANDOFF)) {
+        sm100::mbar_arrive_expect_tx(bar, sizeof(sm.state));
+        sm100::bulk_g2s(sm100::smem_addr(sm.state), state, sizeof(sm.state), bar);
+      }
     }
   }
   const T* qs = reinterpret_cast<const T*>(p.q) + ((size_t)m0 * p.Hk + kh) * dk;
@@ -249,9 +251,10 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
       }
     }
   }
+  auto state_there = [&] { return sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs); };
   if (!__syncthreads_and(parent >= -1 && parent < mine)) {
     if constexpr (kFull && kStaged<kNodes>) {  // the copy in flight writes to this CTA's memory
-      if (!sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+      if (!state_there()) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
     }
     if (tid == 0) report(p.status, KDA_ERR_DEVICE_CHECK);
     return;
@@ -311,9 +314,8 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
   // 16 warp + 2 (lane / 4) + {0, 1}) over all key channels.  Within each 16 channels a lane's four
   // are 4 (lane % 4) .. + 3 in both operands (the order of the summed index is free), so that its
   // share of V_FIRST states and of the factors is one wide access.
-  if constexpr (kFull && kStaged<kNodes>) {
-    if (!sm100::mbar_wait_bounded(sm100::smem_addr(&sm.full), 0, kWaitNs)) report(p.status, KDA_ERR_DEVICE_TIMEOUT);
-  }
+  bool late = false;
+  if constexpr (kFull && kStaged<kNodes>) late = !state_there();
   const float* from = kFull && kStaged<kNodes> ? sm.state : state;
   const int q = lane & 3, gr = lane >> 2;
   auto c0 = [&](int g) { return 16 * (warp + kWarps * g) + 4 * q; };  // a lane's columns of the products
@@ -373,7 +375,14 @@ __global__ void __launch_bounds__(kTreeThreads<kNodes>, kNodes <= 16 ? 4 : kNode
 #pragma unroll
       for (int t = 0; t < 2; ++t) right[ks][t].set(s[t][0], s[t][1], s[t][2], s[t][3]);
     }
-    __syncthreads();  // the factors are there, and the state has been read: u and qs take its place
+    // the factors are there, and the state has been read: u and qs take its place
+    if (__syncthreads_or(late)) {  // not the whole state: no results, and no end while it may still arrive
+      if (tid == 0) {
+        state_there();
+        report(p.status, KDA_ERR_DEVICE_TIMEOUT);
+      }
+      return;
+    }
     const int tiles = (n + 7) >> 3;
     for (int t = 0; t < tiles; ++t) {
       float big[2][4] = {}, small[2][4] = {};
