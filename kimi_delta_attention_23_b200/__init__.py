@@ -204,19 +204,20 @@ def _stream(stream, device):
 
 
 # The calls that serve single tokens take a few microseconds on the device, so their wrappers have all
-# tensors checked in one go (_check.so, built beside libkda.so); only where something is not as it
-# should be do the functions here look closer and say what it is.
+# tensors checked in one go (_check.so, built beside libkda.so where that can be); only where something is
+# not as it should be, or without it, do the functions here look closer and say what it is.
 def _checker(expectations):
     """A function of the tensors: device number, extents, addresses and types for the C ABI, or None."""
     made = []
 
     def look(*tensors):
         if not made:
-            try:
+            from . import build
+            if build.check_fits():
                 from . import _check
-            except ImportError as e:
-                raise ImportError("_check.so is not built; run kimi_delta_attention_23_b200/build.py") from e
-            made.append(functools.partial(_check.check, _check.make(expectations)))
+                made.append(functools.partial(_check.check, _check.make(expectations)))
+            else:
+                made.append(lambda *tensors: None)
         return made[0](*tensors)
 
     return look
