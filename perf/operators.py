@@ -229,11 +229,9 @@ def _run_own(s):
         grads = kda.kda_glr_bwd(s["dout"], s["x"], *params, s["cu"], kept, s["dfinal"], **kw)
         if c["out"] == "f32":
             # the plain form adds the final states' gradients into an fp32 dout, where the next pass on the
-            # same state finds them; the two go on from the same dout only if this does so too
-            if "at_ends" not in s:
-                some = s["cu"][1:] > s["cu"][:-1]
-                s["at_ends"] = (s["cu"][1:] - 1).clamp_min(0), s["dfinal"] * some[:, None, None]
-            s["dout"].index_add_(0, *s["at_ends"])
+            # same state finds them; the two go on from the same dout only if this does so too, every pass anew
+            first, end = s["cu"][:-1], s["cu"][1:]
+            s["dout"].index_add_(0, (end - 1).clamp_min(0), s["dfinal"] * (end > first)[:, None, None])
         return {"out": out, "pool": s["pool"], **grads}
     if kind == "tree":
         out, deltas = kda.kda_tree_decode(
