@@ -237,12 +237,19 @@ def _need(t, name, dtype, shape, like, index):
     return t.data_ptr()
 
 
+def _extents(shape, name):
+    """The shape, if the C ABI can name its extents: ctypes would cut off their upper bits and say nothing."""
+    if any(n > 2**31 - 1 for n in shape):
+        raise ValueError(f"{name} has shape {tuple(shape)}: an extent beyond 2^31 - 1")
+    return shape
+
+
 def _need_rank(t, name, dtype, rank, like, index):
     """The same for a tensor of which only the number of dimensions is given; returns its shape and address."""
     try:
         shape = t.shape
         if len(shape) == rank and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
-            return shape, t.data_ptr()
+            return _extents(shape, name), t.data_ptr()
     except AttributeError:
         pass
     _dev(t, name, dtype, like.device)
@@ -254,7 +261,7 @@ def _where(t, name, rank):
     try:
         index, shape = t.get_device(), t.shape
         if index >= 0 and len(shape) == rank and t.is_contiguous():
-            return index, shape, t.data_ptr()
+            return index, _extents(shape, name), t.data_ptr()
     except AttributeError:
         pass
     _dev(t, name)

@@ -120,7 +120,7 @@ PyObject* check(PyObject*, PyObject* const* args, Py_ssize_t count) {
         const int64_t extent = sizes[k] - e.dims[k].plus;
         int64_t& b = bound[e.dims[k].symbol];
         if (b < 0) b = extent;
-        if (b != extent || extent < 0) Py_RETURN_NONE;
+        if (b != extent || extent < 0 || extent > INT32_MAX) Py_RETURN_NONE;  // (the C ABI's are 32 bits)
       }
       address[i] = reinterpret_cast<int64_t>(t.data_ptr());
     }
