@@ -635,7 +635,8 @@ __global__ void __launch_bounds__(kThreads, 2) commit_kernel(const TreeArgs p) {
       for (int l = 0; l < length; ++l) {
         const size_t m = m0 + sm.path[l];
         sm.kw[l][tid] = w * load_in(p.k, (m * p.Hk + kh) * dk + tid, p.in_bf16);
-        w *= expf(gate_f32(p.raw_gate[(m * p.Hv + h) * dk + tid], a_log, bias, p.flags & KDA_GATE_SAFE, p.lb));
+        const float g = gate_f32(p.raw_gate[(m * p.Hv + h) * dk + tid], a_log, bias, false, 0.f);
+        w *= expf(p.flags & KDA_GATE_SAFE ? glr::max_nan(g, p.lb) : g);  // as in the tree, not a number stays one
       }
     } else {
       for (int l = 0; l < length; ++l) sm.kw[l][tid] = 0.f;
