@@ -570,6 +570,7 @@ KDA_API kda_status_t kda_tree_commit(const void *k, kda_dtype_t k_dtype, const f
  * be captured.  live [max_slots] int32: nonzero where a slot is in use.  workspace: at least
  * kda_pool_workspace_size(n, max_slots) bytes, 256-byte aligned; calls that may run at once need one
  * each; a copy of up to 256 pairs needs none.  Entries of -1 in the lists (both, for a copy) are padding.
+ * Lists, and the pools of all calls but the copy, have at most 2^31 - 1025 entries.
  *
  * kda_pool_copy     slot dst[i] = slot src[i] for all i at once: sources are read as they were before
  *                   the call, whatever the order.  A destination named again is reported and only its

@@ -12,6 +12,7 @@ constexpr uint32_t kGlrFlags = kGlrDecodeFlags | KDA_DEBUG_WITHHOLD_HANDOFF;
 constexpr uint32_t kTreeFlags = KDA_GATE_SAFE | KDA_BETA_PROB | KDA_STATE_V_FIRST | KDA_DEBUG_WITHHOLD_HANDOFF;
 constexpr int64_t kMaxTokens = INT32_MAX - 1024;  // the recurrence counts in whole tiles past the end
 constexpr int32_t kMaxNodes = 64;
+constexpr int32_t kMaxEntries = INT32_MAX - 1024;  // of a list or a pool that a plan's 1024 threads walk
 constexpr int32_t kMaxCopies = 8192;  // pairs of one simultaneous copy: 16 bytes of each fit shared memory
 
 bool dtype_ok(kda_dtype_t t) { return t == KDA_F32 || t == KDA_BF16; }
@@ -295,6 +296,7 @@ namespace {
 
 kda_status_t pool_call(kda::PoolArgs& a, kda::PoolOp op, void* workspace, size_t workspace_bytes, void* stream) {
   if (!a.pool || a.layers <= 0 || a.max_slots <= 0 || a.slot_elems <= 0 || a.n < 0) return KDA_ERR_INVALID_ARG;
+  if (a.n > kMaxEntries || (op != kda::kPoolCopy && a.max_slots > kMaxEntries)) return KDA_ERR_INVALID_ARG;
   // element offsets within the stack are 64-bit; their product must be one too
   if (a.slot_elems > INT64_MAX / 4 / a.layers / a.max_slots) return KDA_ERR_INVALID_ARG;
   if (kda::pool_needs_work(op, a.n) &&
