@@ -36,7 +36,7 @@ kda_status_t glr_types(kda_dtype_t x, kda_dtype_t gate, kda_dtype_t out) {
 }
 
 size_t glr_partial_bytes(int64_t T, int32_t batch, int32_t H, int32_t d) {
-  if (T < 0 || T > kMaxTokens || batch <= 0 || H <= 0 || d <= 0 || d > 128) return 0;
+  if (T < 0 || T > kMaxTokens || batch <= 0 || H <= 0 || d <= 0 || d > 128 || !fits(batch, H, 16)) return 0;
   return (size_t)kda::glr_bwd_partials(batch, T, H) * H * (d + 1) * sizeof(float);
 }
 
