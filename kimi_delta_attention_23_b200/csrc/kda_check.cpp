@@ -24,7 +24,6 @@ struct Dim {
 struct Entry {
   char type;      // f float32, i int32, v float32 or bfloat16 (the main type), s the main type, g float32 or,
                   // beside a bfloat16 main type, bfloat16
-  bool optional;  // None allowed: address 0
   std::vector<Dim> dims;
 };
 struct Checker {
@@ -37,7 +36,7 @@ const char* kName = "kda_checker";
 Checker* checker_of(PyObject* o) { return static_cast<Checker*>(PyCapsule_GetPointer(o, kName)); }
 void destroy(PyObject* o) { delete checker_of(o); }
 
-// make("x v T,H,d; cu i B+1; final ?f B,H,d") -> checker
+// make("x v T,H,d; cu i B+1; final f B,H,d") -> checker
 PyObject* make(PyObject*, PyObject* arg) {
   const char* text = PyUnicode_AsUTF8(arg);
   if (!text) return nullptr;
@@ -48,7 +47,7 @@ PyObject* make(PyObject*, PyObject* arg) {
     std::stringstream words(item);
     std::string name, type, dims, dim;
     words >> name >> type >> dims;
-    Entry e{type.back(), type[0] == '?', {}};
+    Entry e{type.size() == 1 ? type[0] : ' ', {}};
     std::stringstream list(dims);
     while (std::getline(list, dim, ',')) {
       int64_t plus = 0;
@@ -93,10 +92,6 @@ PyObject* check(PyObject*, PyObject* const* args, Py_ssize_t count) {
     for (int i = 0; i < n; ++i) {
       const Entry& e = c->entries[i];
       PyObject* o = args[i + 1];
-      if (o == Py_None && e.optional) {
-        address[i] = 0;
-        continue;
-      }
       if (!THPVariable_Check(o)) Py_RETURN_NONE;
       const at::Tensor& t = THPVariable_Unpack(o);
       if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() != (int64_t)e.dims.size() || !t.is_contiguous()) Py_RETURN_NONE;

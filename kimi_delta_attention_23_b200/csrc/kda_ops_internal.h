@@ -54,7 +54,7 @@ struct GlrBwdArgs {
   float* da_log;             // [H]
   float* ddt_bias;           // [H,d]
   float* d_initial;          // [batch][H][d]
-  float* partial;            // glr_bwd_partials() x [H][d] and then x [H]
+  float* partial;            // glr_bwd_partials() x [H][d + 1]: a head's sums over its channels' bias and gate
   uint32_t flags;
   float lb;
   int32_t* status;
