@@ -473,8 +473,8 @@ KDA_API int32_t kda_version(void);
  * Types: x F32 with gate F32 and out F32; or x BF16 with gate BF16 or F32 and out BF16 or F32.
  * 1 <= d <= 128; total_tokens at most 2^31 - 1025.  Any alignment of whole elements; rows of a multiple of four channels on 16-byte
  * (bf16: 8-byte) boundaries are read and written in wide accesses.
- * flags: KDA_GATE_SAFE, KDA_BETA_PROB, KDA_INPUT_NORM.  Arithmetic and states in fp32; results do
- * not depend on timing.
+ * flags: KDA_GATE_SAFE (with gate_lower_bound <= 0), KDA_BETA_PROB, KDA_INPUT_NORM.  Arithmetic and
+ * states in fp32; results do not depend on timing.
  */
 KDA_API kda_status_t kda_glr_fwd(const void *x, kda_dtype_t x_dtype, const void *raw_gate,
                                  kda_dtype_t gate_dtype, const float *beta_logits, const float *a_log,
@@ -538,7 +538,8 @@ KDA_API size_t kda_glr_bwd_workspace_size(int64_t total_tokens, int32_t batch, i
  *          along its key; kda_tree_commit reads them
  *   max_nodes (1 .. 64): no sequence drafts more; one that does is reported and skipped, as are
  *          bad offsets, a bad slot and a parent outside [-1, node)
- * Types and head sizes as kda_decode; fp32-accurate arithmetic.
+ * Types and head sizes as kda_decode; fp32-accurate arithmetic, whatever the types.  KDA_GATE_SAFE
+ * takes gate_lower_bound <= 0, here and in the commit.
  */
 KDA_API kda_status_t kda_tree_decode(const void *q, const void *k, const void *v, kda_dtype_t qkv_dtype,
                                      const float *raw_gate, const float *beta_logits, const float *a_log,

@@ -26,6 +26,8 @@ cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 bool work_ok(const void* p, size_t have, size_t need) {
   return need == 0 || (p && have >= need && !(reinterpret_cast<uintptr_t>(p) & 255u));
 }
+// A safe gate's bound is a logarithm of a decay: the kernels' exponential is made for gates of at most 0.
+bool bound_ok(uint32_t flags, float lb) { return !(flags & KDA_GATE_SAFE) || lb <= 0.f; }
 // grid sizes and per-call element counts of the kernels
 bool fits(int64_t batch, int64_t heads, int64_t each) { return batch * heads <= INT32_MAX / each; }
 
@@ -55,7 +57,7 @@ extern "C" kda_status_t kda_glr_fwd(const void* x, kda_dtype_t x_dtype, const vo
                                     int32_t* device_status, void* stream) {
   if (batch < 0 || total_tokens < 0 || total_tokens > kMaxTokens || num_heads <= 0 || d <= 0 || max_slots <= 0)
     return KDA_ERR_INVALID_ARG;
-  if ((flags & ~kGlrFlags) != 0) return KDA_ERR_INVALID_ARG;
+  if ((flags & ~kGlrFlags) != 0 || !bound_ok(flags, gate_lower_bound)) return KDA_ERR_INVALID_ARG;
   if (!cu_seqlens || !state_pool || !state_indices || !a_log || !dt_bias) return KDA_ERR_INVALID_ARG;
   if (total_tokens > 0 && (!x || !raw_gate || !beta_logits || !out)) return KDA_ERR_INVALID_ARG;
   if (kda_status_t s = glr_types(x_dtype, gate_dtype, out_dtype); s != KDA_OK) return s;
@@ -94,7 +96,7 @@ extern "C" kda_status_t kda_glr_decode(const void* x, kda_dtype_t x_dtype, const
                                        kda_dtype_t out_dtype, uint32_t flags, float gate_lower_bound,
                                        int32_t* device_status, void* stream) {
   if (batch < 0 || num_heads <= 0 || d <= 0 || max_slots <= 0) return KDA_ERR_INVALID_ARG;
-  if ((flags & ~kGlrDecodeFlags) != 0) return KDA_ERR_INVALID_ARG;
+  if ((flags & ~kGlrDecodeFlags) != 0 || !bound_ok(flags, gate_lower_bound)) return KDA_ERR_INVALID_ARG;
   if (!state_pool || !state_indices || !a_log || !dt_bias) return KDA_ERR_INVALID_ARG;
   if (batch > 0 && (!x || !raw_gate || !beta_logits || !out)) return KDA_ERR_INVALID_ARG;
   if (kda_status_t s = glr_types(x_dtype, gate_dtype, out_dtype); s != KDA_OK) return s;
@@ -137,7 +139,7 @@ extern "C" kda_status_t kda_glr_bwd(const void* dout, kda_dtype_t out_dtype, con
                                     float gate_lower_bound, void* workspace, size_t workspace_bytes,
                                     int32_t* device_status, void* stream) {
   if (batch < 0 || total_tokens < 0 || total_tokens > kMaxTokens || num_heads <= 0 || d <= 0) return KDA_ERR_INVALID_ARG;
-  if ((flags & ~kGlrFlags) != 0) return KDA_ERR_INVALID_ARG;
+  if ((flags & ~kGlrFlags) != 0 || !bound_ok(flags, gate_lower_bound)) return KDA_ERR_INVALID_ARG;
   if (!cu_seqlens || !a_log || !dt_bias || !da_log || !ddt_bias) return KDA_ERR_INVALID_ARG;
   if (batch > 0 && (!d_initial || !checkpoints)) return KDA_ERR_INVALID_ARG;
   if (total_tokens > 0 && (!dout || !x || !raw_gate || !beta_logits || !dx || !draw_gate || !dbeta))
@@ -187,11 +189,11 @@ namespace {
 
 // what the two calls on trees check alike
 kda_status_t tree_checks(int32_t batch, int64_t total_nodes, int32_t max_nodes, int32_t Hk, int32_t Hv, int32_t dk,
-                         int32_t dv, int32_t max_slots, uint32_t flags) {
+                         int32_t dv, int32_t max_slots, uint32_t flags, float lb) {
   if (batch < 0 || total_nodes < 0 || total_nodes > INT32_MAX || max_nodes <= 0 || Hk <= 0 || Hv <= 0 || dk <= 0 ||
       dv <= 0 || max_slots <= 0)
     return KDA_ERR_INVALID_ARG;
-  if (Hv % Hk != 0 || (flags & ~kTreeFlags) != 0) return KDA_ERR_INVALID_ARG;
+  if (Hv % Hk != 0 || (flags & ~kTreeFlags) != 0 || !bound_ok(flags, lb)) return KDA_ERR_INVALID_ARG;
   if (!fits(batch, Hv, 1)) return KDA_ERR_INVALID_ARG;
   if (dk > 128 || dv > 128 || max_nodes > kMaxNodes) return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
@@ -207,7 +209,8 @@ extern "C" kda_status_t kda_tree_decode(const void* q, const void* k, const void
                                         int32_t max_slots, const int32_t* state_indices, void* out,
                                         kda_dtype_t out_dtype, float* deltas, uint32_t flags, float gate_lower_bound,
                                         int32_t* device_status, void* stream) {
-  const kda_status_t st = tree_checks(batch, total_nodes, max_nodes, num_k_heads, num_v_heads, dk, dv, max_slots, flags);
+  const kda_status_t st = tree_checks(batch, total_nodes, max_nodes, num_k_heads, num_v_heads, dk, dv, max_slots, flags,
+                                      gate_lower_bound);
   if (st == KDA_ERR_INVALID_ARG) return st;
   if (!cu_nodes || !state_pool || !state_indices || !a_log || !dt_bias) return KDA_ERR_INVALID_ARG;
   if (total_nodes > 0 && (!q || !k || !v || !raw_gate || !beta_logits || !parents || !out || !deltas))
@@ -254,7 +257,8 @@ extern "C" kda_status_t kda_tree_commit(const void* k, kda_dtype_t k_dtype, cons
                                         int32_t num_v_heads, int32_t dk, int32_t dv, float* state_pool,
                                         int32_t max_slots, const int32_t* state_indices, uint32_t flags,
                                         float gate_lower_bound, int32_t* device_status, void* stream) {
-  const kda_status_t st = tree_checks(batch, total_nodes, max_nodes, num_k_heads, num_v_heads, dk, dv, max_slots, flags);
+  const kda_status_t st = tree_checks(batch, total_nodes, max_nodes, num_k_heads, num_v_heads, dk, dv, max_slots, flags,
+                                      gate_lower_bound);
   if (st == KDA_ERR_INVALID_ARG) return st;
   if (!cu_nodes || !state_pool || !state_indices || !a_log || !dt_bias || !accepted) return KDA_ERR_INVALID_ARG;
   if (total_nodes > 0 && (!k || !raw_gate || !parents || !deltas)) return KDA_ERR_INVALID_ARG;
