@@ -237,9 +237,12 @@ def _need(t, name, dtype, shape, like, index):
     return t.data_ptr()
 
 
+_MOST = 2**31 - 1  # what an extent of the C ABI can be: ctypes would cut off its upper bits and say nothing
+
+
 def _extents(shape, name):
-    """The shape, if the C ABI can name its extents: ctypes would cut off their upper bits and say nothing."""
-    if any(n > 2**31 - 1 for n in shape):
+    """The shape, if the C ABI can name its extents."""
+    if max(shape) > _MOST:
         raise ValueError(f"{name} has shape {tuple(shape)}: an extent beyond 2^31 - 1")
     return shape
 
@@ -289,13 +292,13 @@ def _launch(index, call, *args):
 # and scratch) is allocated with ``stream`` current; and the results, which the caller goes on to use on its
 # own current stream, are marked as in use there (``record_stream``), so that freeing them waits for both.
 def _elsewhere(stream, device):
-    """Whether the call's kernels run on another stream than the current one."""
-    return stream is not None and stream != torch.cuda.current_stream(device)
+    """Whether ``stream``, which a call was given, is another than the current one."""
+    return stream != torch.cuda.current_stream(device)
 
 
 def _make(stream, device, make, /, *args, **kw):
     """make(...), a tensor that kernels on ``stream`` may write at once."""
-    if not _elsewhere(stream, device):
+    if stream is None or not _elsewhere(stream, device):
         return make(*args, **kw)
     with torch.cuda.stream(stream):
         return make(*args, **kw)
@@ -303,7 +306,7 @@ def _make(stream, device, make, /, *args, **kw):
 
 def _hand_over(stream, device, *tensors):
     """Results of _make that the caller gets, on its way out of the call."""
-    if _elsewhere(stream, device):
+    if stream is not None and _elsewhere(stream, device):
         current = torch.cuda.current_stream(device)
         for t in tensors:
             if t is not None and t.numel():

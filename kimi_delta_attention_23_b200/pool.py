@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import KdaError, _dev, _extents, _hand_over, _launch, _make, _need, _need_rank, _on_stream, load_library
+from . import KdaError, _MOST, _dev, _extents, _hand_over, _launch, _make, _need, _need_rank, _on_stream, load_library
 
 __all__ = ["kda_pool_copy", "kda_pool_fork", "kda_pool_free", "kda_pool_compact", "kda_pool_workspace_size",
            "MAX_POOL_COPIES"]
@@ -42,7 +42,9 @@ def _layout(pool, stacked):
         _dev(pool, "state_pool", torch.float32)
         raise ValueError(f"state_pool has shape {tuple(shape)}, expected "
                          f"{'[layers, slots, ...]' if stacked else '[slots, ...]'} with at least one element")
-    layers, slots = _extents(shape[:2], "state_pool") if stacked else (1, *_extents(shape[:1], "state_pool"))
+    layers, slots = (shape[0], shape[1]) if stacked else (1, shape[0])
+    if slots > _MOST or layers > _MOST:
+        _extents((layers, slots), "state_pool")
     return pool, pool.get_device(), layers, slots, pool.numel() // (layers * slots)
 
 
