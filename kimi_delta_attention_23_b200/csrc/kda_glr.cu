@@ -19,10 +19,12 @@
 // over the cluster's tiles through distributed shared memory.  Every CTA folds the same maps in the
 // same order, so results do not depend on timing, and the carry never goes through global memory.
 //
-// Measured (B200, H = 32, d = 128): forward, 131072 tokens in bf16 with the normalised input, 0.905 ms for
-// 3.24 GB (3.6 TB/s, 55 % of the copy rate): 128 of the 148 SMs work (32 heads x 4 CTAs), at 68 % of their
-// issue slots.  32768 packed tokens with fp32 gates: forward 0.250 ms (1.07 GB), backward 0.575 ms (1.88 GB,
-// 50 %), where 16 warps in step leave issue slots empty behind waits and shared-memory latency.
+// Measured (B200, H = 32, d = 128): forward, 131072 tokens in bf16 with the normalised input, 0.912 ms for
+// 3.24 GB (3.6 TB/s, 54 % of the copy rate): 128 of the 148 SMs work (32 heads x 4 CTAs), at 68 % of their
+// issue slots.  32768 packed tokens with fp32 gates: forward 0.252 ms (1.07 GB), backward 0.589 ms (1.88 GB,
+// 49 %), where 16 warps in step leave issue slots empty behind waits and shared-memory latency.  With the
+// normalised input the backward pass takes 0.88 ms, in bf16 throughout 0.89: it works the decay and the root
+// out anew for the maps, the states and the gradients, and spills.
 //
 // The backward pass walks the tiles in reverse.  The forward pass has kept the state entering each
 // tile (1/64 of the fp32 size of the outputs), so h_{t-1} is rebuilt inside the tile and only D is
@@ -963,8 +965,10 @@ bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 
 // CTAs per (sequence, head).  One fits an SM at a time, so c of them make ceil(chains c / SMs) rounds of
 // 1 / c of a chain; sequences of unequal lengths leave about one more round half empty, and each CTA of a
-// cluster adds some 4 % to a step.  8 packed sequences of 32 heads (32768 tokens, forward / backward): 1 CTA
-// 272 / 774 us, 2: 243 / 685, 4: 246 / 666, 8: 306 / 666; one of 131072 tokens: 4 989 us, 8 1437 us.
+// cluster adds some 4 % to a step.  One sequence of 131072 tokens and 32 heads, forward / backward: 1 CTA
+// 3569 / 14306 us, 2: 1801 / 7124, 4: 919 / 3426, 8: 1407 / 5146; the rule
+// takes 4.  8 packed sequences (32768 tokens): 1: 297 / 761, 2: 225 / 554, 4 (4 at most backwards): 251 / 589, 8: 325;
+// the rule takes 4 here too, 11 % and 6 % above the best.
 int cluster_size(int32_t batch, int64_t T, int32_t H, int most) {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

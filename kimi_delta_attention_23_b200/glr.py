@@ -12,6 +12,10 @@ sequence, head, channel and token
 with beta = sigmoid(beta_logits), or beta_logits itself with beta_mode "probability".  Types: x float32
 with raw_gate and out float32; or x bfloat16 with raw_gate and out each bfloat16 or float32.  States,
 parameters, beta and the sums over tokens are float32.
+
+Autograd does not see these calls: what kda_glr_fwd returns has no history, also where its inputs require
+gradients.  Those come from kda_glr_bwd, called with the gradient of the outputs (a torch.autograd.Function
+of the two makes them one operation of a model).
 """
 from __future__ import annotations
 
