@@ -33,9 +33,9 @@
 #include <cuda.h>
 #include <cstddef>
 
+#include "kda_cluster.cuh"
 #include "kda_glr_math.cuh"
 #include "kda_ops_internal.h"
-#include "kda_sm100.cuh"
 
 namespace kda {
 namespace {
